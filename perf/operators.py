@@ -345,7 +345,7 @@ def _plain_route(st, dtype=torch.float32):
     loss = (E * (share * mean_p).sum()).to(dtype).reshape(1)
     out = {"expert_index": torch.where(chosen, idx, -1).to(torch.int32), "weights": w,
            "counts": counts.to(torch.int32), "m_offsets": off, "row_index": row_index,
-           "pair_row": pair_row.view(T, k), "loss": loss}
+           "pair_row": pair_row.view(T, k), "routed": n.to(torch.int32).reshape(1), "loss": loss}
     if st["train"]:
         dl, dw = st["d_loss"].to(dtype), torch.where(chosen, st["d_weights"].to(dtype), 0.0)
         dp = (dl * E * share.to(dtype) / n.clamp_min(1.0).to(dtype)).expand(T, E)
