@@ -275,6 +275,166 @@ int nvfp4_mxfp4_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a_q, const 
                      const uint8_t* b_q, const uint8_t* b_s, void* y, nvfp4_dtype y_dtype,
                      int64_t ld_y, void* stream);
 
+/*
+ * FP8 operands: E4M3FN bytes with one fp32 scale per block of 128 elements
+ * of K, for the layers a 4-bit format is too coarse for and for training.
+ *   q  uint8 [rows, K]   E4M3FN bit patterns, dense rows
+ *   s  fp32  [ceil(K/128), ceil(rows/block_rows)]
+ *      block_rows 1: a scale per row and block; block_rows 128: per 128 x 128
+ *   an element decodes as E4M3(q[r, k]) * s[k / 128, r / block_rows]
+ * The last block of a row (of 128 rows) may be shorter.
+ *
+ * nvfp4_fp8_quantize: x [batch, rows, cols] (matrix b starts at row b * rows,
+ * row stride ld_x elements, F32 or BF16) -> either or both of
+ *   rows layout  q [batch, rows, cols], s of blocks along the rows: the
+ *                operand of a product over cols;
+ *   transposed   qt [batch, cols, rows_t], st of blocks along the columns,
+ *                rows_t = rows rounded up to 16 (bytes past rows are zero):
+ *                the operand of a product over rows, as the gradients need.
+ * Per block: A = max(max|x|, 2^-100), s = fl32(A / 448), and each byte is the
+ * E4M3 rounding (nearest, ties to even) of fl32(x * fl32(448 / A)).  A block
+ * holding a NaN or an infinity gets a NaN scale and zero bytes.  With
+ * block_rows 128 both layouts hold the same values.  One pass over x, no
+ * workspace, deterministic.
+ * Errors: NVFP4_ERR_INVALID_ARG for cols % 16 != 0, block_rows not 1 or 128,
+ * negative sizes, a bad dtype, ld_x < cols, one pointer of a pair (q, s) or
+ * (qt, st) without the other, both pairs null, or a null x;
+ * NVFP4_ERR_UNSUPPORTED for x, its rows, q or qt not 16-byte aligned, or a
+ * dimension above 2^30.
+ */
+int nvfp4_fp8_quantize(const void* x, nvfp4_dtype x_dtype, int64_t batch, int64_t rows,
+                       int64_t cols, int64_t ld_x, int block_rows, uint8_t* q, float* s,
+                       uint8_t* qt, float* st, void* stream);
+
+/* Columns P of an expert-wise transposed operand of total_m tokens in G
+ * groups (below): 128 * floor((total_m + 127 * min(G, total_m)) / 128). */
+int64_t nvfp4_fp8_grouped_columns(int64_t total_m, int32_t G);
+
+/*
+ * The same quantisation (block_rows 1) of rows sorted by group, m_offsets as
+ * in nvfp4_grouped_gemm (here m_offsets[G] <= total_m; rows of no group are
+ * not read, and q, s are left as they were there):
+ *   rows layout  q [total_m, cols], s [ceil(cols/128), total_m]
+ *   transposed   qt [cols, P], st [P/128, cols]: each group's tokens start at
+ *                the next multiple of 128 columns, so that no block mixes
+ *                groups; columns of no token are zero.
+ * row_index (or NULL): grouped row r is row row_index[r] of x [x_rows, cols];
+ * an index outside [0, x_rows) is a row of zeros.  Without it x has total_m
+ * rows and x_rows is not read.  Errors as above.
+ */
+int nvfp4_fp8_grouped_quantize(const void* x, nvfp4_dtype x_dtype, int32_t G,
+                               const int32_t* m_offsets, const int32_t* row_index,
+                               int64_t total_m, int64_t x_rows, int64_t cols, int64_t ld_x,
+                               uint8_t* q, float* s, uint8_t* qt, float* st, void* stream);
+
+/* nvfp4_fp8_gemm / nvfp4_fp8_grouped_wgrad flag: y += product (F32 y). */
+#define NVFP4_ACCUMULATE 1u
+
+/*
+ * y[m, n] (+)= sum_k A(m, k) * B(n, k) of FP8 operands a [M, K] (block_rows 1)
+ * and b [N, K] (b_block_rows 1 or 128).  A linear layer's three products:
+ *   y  = x . W^T       a = x (rows),           b = W (128, rows)
+ *   dx = dy . W        a = dy (rows),          b = W (128, transposed)
+ *   dW = dy^T . x      a = dy (transposed),    b = x (transposed)
+ * Each block's products are summed in fp32 and scaled by the two fp32 scales
+ * as they are added to the fp32 result (sa * sb must be finite).
+ * y [M, N] has row stride ld_y >= N elements.  A NaN scale gives NaN in the
+ * rows (columns) it scales.  K == 0 writes zeros (adds nothing).
+ * Errors: NVFP4_ERR_INVALID_ARG for K % 16 != 0, b_block_rows not 1 or 128,
+ * negative sizes, a bad dtype or flag, NVFP4_ACCUMULATE with a BF16 y,
+ * ld_y < N or a null pointer; NVFP4_ERR_UNSUPPORTED for q not 16-byte
+ * aligned, s or y not aligned to their elements, K > 2^22 or another
+ * dimension above 2^30.
+ */
+int nvfp4_fp8_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a_q, const float* a_s,
+                   const uint8_t* b_q, const float* b_s, int b_block_rows, void* y,
+                   nvfp4_dtype y_dtype, int64_t ld_y, unsigned flags, void* stream);
+
+/*
+ * Experts' products: group e's rows of a times its own weight
+ * (b_q + e*N*K, b_s [G, ceil(K/128), ceil(N/128)]), as nvfp4_grouped_gemm and
+ * (with row_index, a [a_rows, K]) nvfp4_grouped_gemm_gather; here
+ * m_offsets[G] <= total_m is allowed, and rows of y of no group are left as
+ * they were.  Without row_index a has total_m rows and a_rows must be 0 or
+ * total_m.  The input gradient is the same call with dy and the transposed
+ * weights.  Errors as nvfp4_fp8_gemm, and NVFP4_ERR_UNSUPPORTED for
+ * a_rows * K >= 2^31 with row_index.
+ */
+int nvfp4_fp8_grouped_gemm(int32_t G, const int32_t* m_offsets, const int32_t* row_index,
+                           int64_t total_m, int64_t a_rows, int64_t N, int64_t K,
+                           const uint8_t* a_q, const float* a_s, const uint8_t* b_q,
+                           const float* b_s, void* y, nvfp4_dtype y_dtype, int64_t ld_y,
+                           void* stream);
+
+/*
+ * Experts' weight gradients: dw[e, n, k] (+)= sum over group e's tokens of
+ * dy[r, n] * x[r, k], from the transposed operands of
+ * nvfp4_fp8_grouped_quantize: a = dy (a_q [N, P], a_s [P/128, N]) and b = x
+ * (b_q [K, P], b_s [P/128, K]), P = nvfp4_fp8_grouped_columns(total_m, G).
+ * dw [G, N, K] is dense; a group without tokens gets zeros (is left alone
+ * with NVFP4_ACCUMULATE).  N, K >= 0 of any size.  Errors as nvfp4_fp8_gemm
+ * (P in the place of K).
+ */
+int nvfp4_fp8_grouped_wgrad(int32_t G, const int32_t* m_offsets, int64_t total_m, int64_t N,
+                            int64_t K, const uint8_t* a_q, const float* a_s, const uint8_t* b_q,
+                            const float* b_s, void* dw, nvfp4_dtype dw_dtype, unsigned flags,
+                            void* stream);
+
+/* nvfp4_moe_route flag: weights are the softmax over the chosen experts. */
+#define NVFP4_ROUTE_RENORMALIZE 1u
+
+/* Bytes of device workspace of nvfp4_moe_route. */
+size_t nvfp4_moe_route_workspace_bytes(int64_t T, int64_t E);
+
+/*
+ * Router of a mixture of experts: logits [T, E] (F32 or BF16, row stride
+ * ld_logits elements) -> for each token its topk experts, and what the
+ * grouped GEMMs take.
+ *   p[t, :]      = softmax(logits[t, :])
+ *   expert_index int32 [T, topk]  experts of the largest logits, descending,
+ *                ties to the lowest expert
+ *   weights      fp32 [T, topk]   p at those (or, renormalised, their softmax)
+ *   counts       int32 [E]        tokens of each expert
+ *   m_offsets    int32 [E + 1]    their running sums
+ *   row_index    int32 [T * topk] token of each grouped row, sorted by
+ *                (expert, token); -1 behind m_offsets[E]
+ *   pair_row     int32 [T, topk]  grouped row of each choice
+ *   routed       int32 [1]        n, tokens that chose any expert
+ *   loss         fp32 [1]         E * sum_e (counts_e / (n topk)) (1/n sum_t p[t, e]),
+ *                1 for an even load; 0 when n == 0
+ * token_mask (uint8 [T], or NULL): a token with 0 chooses nothing and counts
+ * nowhere.  An expert at -inf is never chosen; choices that are left over
+ * are expert -1, weight 0, pair_row -1.  Other logits must be finite.
+ * Probabilities and sums are fp32 or wider, in an order that does not change
+ * between calls.  T == 0 writes counts, m_offsets, routed and loss.
+ * workspace >= nvfp4_moe_route_workspace_bytes(T, E) bytes, 4-byte aligned,
+ * not shared by calls that may overlap.
+ * Errors: NVFP4_ERR_INVALID_ARG for T < 0, E < 1, topk < 1 or > E, a bad
+ * dtype or flag, ld_logits < E, a null pointer or a workspace too small;
+ * NVFP4_ERR_UNSUPPORTED for E > 1024, topk > 16, T * topk >= 2^31, or
+ * pointers not aligned to their elements.
+ */
+int nvfp4_moe_route(int64_t T, int64_t E, int32_t topk, const void* logits,
+                    nvfp4_dtype logits_dtype, int64_t ld_logits, const uint8_t* token_mask,
+                    unsigned flags, int32_t* expert_index, float* weights, int32_t* counts,
+                    int32_t* m_offsets, int32_t* row_index, int32_t* pair_row, int32_t* routed,
+                    float* loss, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of the logits of nvfp4_moe_route (same logits, mask and flags, and
+ * its expert_index, counts and routed) from d_weights fp32 [T, topk] and
+ * d_loss fp32 [1] (device; either may be NULL for none).  counts are
+ * constants of the loss.  d_logits [T, E] has the logits' dtype and row
+ * stride ld_d >= E; rows of tokens that chose nothing are zero.  d_weights
+ * of left-over choices are not read.  T == 0 enqueues nothing.
+ */
+int nvfp4_moe_route_backward(int64_t T, int64_t E, int32_t topk, const void* logits,
+                             nvfp4_dtype logits_dtype, int64_t ld_logits,
+                             const uint8_t* token_mask, unsigned flags,
+                             const int32_t* expert_index, const int32_t* counts,
+                             const int32_t* routed, const float* d_weights, const float* d_loss,
+                             void* d_logits, int64_t ld_d, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

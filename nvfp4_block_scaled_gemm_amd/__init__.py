@@ -12,4 +12,10 @@ from ._lib import (  # noqa: F401
     nvfp4_grouped_gemm_multi_raw, nvfp4_grouped_gemm_raw, nvfp4_mxfp4_gemm,
     nvfp4_mxfp4_gemm_raw, nvfp4_mxfp4_quantize, nvfp4_mxfp4_quantize_raw,
     nvfp4_quantize, nvfp4_quantize_noalloc_raw, nvfp4_quantize_raw, nvfp4_quantize_workspace_bytes,
+    Fp8Packed, MoeRoute, NVFP4_ACCUMULATE, NVFP4_ROUTE_RENORMALIZE, nvfp4_fp8_gemm,
+    nvfp4_fp8_gemm_raw, nvfp4_fp8_grouped_columns, nvfp4_fp8_grouped_gemm,
+    nvfp4_fp8_grouped_gemm_raw, nvfp4_fp8_grouped_quantize, nvfp4_fp8_grouped_quantize_raw,
+    nvfp4_fp8_grouped_wgrad, nvfp4_fp8_grouped_wgrad_raw, nvfp4_fp8_quantize,
+    nvfp4_fp8_quantize_raw, nvfp4_moe_route, nvfp4_moe_route_backward,
+    nvfp4_moe_route_backward_raw, nvfp4_moe_route_raw, nvfp4_moe_route_workspace_bytes,
 )

@@ -10,6 +10,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import typing
 
 import torch
 
@@ -27,7 +28,12 @@ NVFP4_GLOBAL_SCALE_GIVEN = 1
 EXPORTED = ("nvfp4_status_string", "nvfp4_version", "nvfp4_quantize_workspace_bytes",
             "nvfp4_quantize", "nvfp4_quantize_noalloc", "nvfp4_gemm", "nvfp4_gemm_nvfp4_out", "nvfp4_grouped_gemm",
             "nvfp4_grouped_gemm_gather", "nvfp4_grouped_gemm_multi", "nvfp4_mxfp4_quantize",
-            "nvfp4_mxfp4_gemm")
+            "nvfp4_mxfp4_gemm", "nvfp4_fp8_quantize", "nvfp4_fp8_grouped_columns",
+            "nvfp4_fp8_grouped_quantize", "nvfp4_fp8_gemm", "nvfp4_fp8_grouped_gemm",
+            "nvfp4_fp8_grouped_wgrad", "nvfp4_moe_route_workspace_bytes", "nvfp4_moe_route",
+            "nvfp4_moe_route_backward")
+NVFP4_ACCUMULATE = 1
+NVFP4_ROUTE_RENORMALIZE = 1
 NVFP4_GROUPED_MAX_PROBLEMS = 4
 
 _lib = None
@@ -87,6 +93,29 @@ def load() -> ctypes.CDLL:
     lib.nvfp4_mxfp4_quantize.restype = ctypes.c_int
     lib.nvfp4_mxfp4_gemm.argtypes = [i64, i64, i64, p, p, p, p, p, ctypes.c_int, i64, p]
     lib.nvfp4_mxfp4_gemm.restype = ctypes.c_int
+    c_int, c_uint = ctypes.c_int, ctypes.c_uint
+    lib.nvfp4_fp8_quantize.argtypes = [p, c_int, i64, i64, i64, i64, c_int, p, p, p, p, p]
+    lib.nvfp4_fp8_quantize.restype = c_int
+    lib.nvfp4_fp8_grouped_columns.argtypes = [i64, i32]
+    lib.nvfp4_fp8_grouped_columns.restype = i64
+    lib.nvfp4_fp8_grouped_quantize.argtypes = [p, c_int, i32, p, p, i64, i64, i64, i64, p, p, p, p,
+                                               p]
+    lib.nvfp4_fp8_grouped_quantize.restype = c_int
+    lib.nvfp4_fp8_gemm.argtypes = [i64, i64, i64, p, p, p, p, c_int, p, c_int, i64, c_uint, p]
+    lib.nvfp4_fp8_gemm.restype = c_int
+    lib.nvfp4_fp8_grouped_gemm.argtypes = [i32, p, p, i64, i64, i64, i64, p, p, p, p, p, c_int, i64,
+                                           p]
+    lib.nvfp4_fp8_grouped_gemm.restype = c_int
+    lib.nvfp4_fp8_grouped_wgrad.argtypes = [i32, p, i64, i64, i64, p, p, p, p, p, c_int, c_uint, p]
+    lib.nvfp4_fp8_grouped_wgrad.restype = c_int
+    lib.nvfp4_moe_route_workspace_bytes.argtypes = [i64, i64]
+    lib.nvfp4_moe_route_workspace_bytes.restype = sz
+    lib.nvfp4_moe_route.argtypes = [i64, i64, i32, p, c_int, i64, p, c_uint, p, p, p, p, p, p, p, p,
+                                    p, sz, p]
+    lib.nvfp4_moe_route.restype = c_int
+    lib.nvfp4_moe_route_backward.argtypes = [i64, i64, i32, p, c_int, i64, p, c_uint, p, p, p, p, p,
+                                             p, i64, p]
+    lib.nvfp4_moe_route_backward.restype = c_int
     _lib = lib
     return lib
 
@@ -491,3 +520,392 @@ def nvfp4_mxfp4_gemm(a, b, out_dtype: str = "bf16", y: torch.Tensor | None = Non
                                   code, ld_y, _stream(None, da))
     _check("nvfp4_mxfp4_gemm", st)
     return y
+
+
+# --------------------------------------------------------------------------
+# FP8 operands (E4M3 bytes, one fp32 scale per 128 elements of a row or per
+# 128 x 128 block)
+# --------------------------------------------------------------------------
+
+_F8 = torch.float8_e4m3fn
+
+
+def _on_gpu(dev: int):
+    """Context in which the library launches on GPU ``dev``."""
+    return contextlib.nullcontext() if torch.cuda.current_device() == dev else torch.cuda.device(dev)
+
+
+def _stride(t, cols: int, what: str) -> int:
+    """Row stride of a 2-D tensor whose rows must be contiguous (a single
+    row's stride says nothing, so its length stands in)."""
+    _need(t.stride(-1) == 1 or cols <= 1, f"{what}: rows must have unit column stride")
+    return t.stride(-2) if t.shape[-2] > 1 else cols
+
+
+class Fp8Packed(tuple):
+    """(q, s) of an FP8 operand [rows, K], or of G of them [G, rows, K]:
+    float8_e4m3fn q and fp32 s [.., ceil(K/128), ceil(rows/block_rows)], both
+    contiguous, on one GPU; block_rows is 1 or 128, told by s's shape.
+    Checked when made; nvfp4_fp8_quantize returns one."""
+
+    def __new__(cls, ts):
+        q, s = ts
+        self = super().__new__(cls, (q, s))
+        _need(q.dtype == _F8 and s.dtype == torch.float32, "q must be float8_e4m3fn and s fp32")
+        _need(2 <= q.dim() <= 3 and s.dim() == q.dim(), "q and s: 2-D, or 3-D with one per matrix")
+        shape, rows, K = tuple(q.shape), q.shape[-2], q.shape[-1]
+        _need(K % 16 == 0, f"q {shape}: K must be a multiple of 16")
+        head, n = (*shape[:-2], -(-K // 128)), s.shape[-1]
+        _need(tuple(s.shape[:-1]) == head and n in (rows, -(-rows // 128)),
+              f"q {shape} and s {tuple(s.shape)} do not belong together")
+        _need(q.is_contiguous() and s.is_contiguous(), "q and s must be contiguous")
+        dev = q.get_device()
+        _need(q.is_cuda and s.get_device() == dev, "q and s must be on one GPU")
+        self.lead, self.rows, self.K, self.dev = shape[:-2], rows, K, dev
+        self.block_rows = 1 if n == rows else 128
+        return self
+
+
+def _fp8(t2) -> Fp8Packed:
+    return t2 if type(t2) is Fp8Packed else Fp8Packed(t2)
+
+
+def nvfp4_fp8_quantize_raw(x, x_dtype, batch, rows, cols, ld_x, block_rows, q, s, qt, st,
+                           stream=None) -> int:
+    return load().nvfp4_fp8_quantize(x, x_dtype, batch, rows, cols, ld_x, block_rows, q, s, qt, st,
+                                     _stream(stream))
+
+
+def nvfp4_fp8_grouped_columns(total_m: int, G: int) -> int:
+    return int(load().nvfp4_fp8_grouped_columns(total_m, G))
+
+
+def nvfp4_fp8_grouped_quantize_raw(x, x_dtype, G, m_offsets, row_index, total_m, x_rows, cols, ld_x,
+                                   q, s, qt, st, stream=None) -> int:
+    return load().nvfp4_fp8_grouped_quantize(x, x_dtype, G, m_offsets, row_index, total_m, x_rows,
+                                             cols, ld_x, q, s, qt, st, _stream(stream))
+
+
+def nvfp4_fp8_gemm_raw(M, N, K, a_q, a_s, b_q, b_s, b_block_rows, y, y_dtype, ld_y, flags,
+                       stream=None) -> int:
+    return load().nvfp4_fp8_gemm(M, N, K, a_q, a_s, b_q, b_s, b_block_rows, y, y_dtype, ld_y, flags,
+                                 _stream(stream))
+
+
+def nvfp4_fp8_grouped_gemm_raw(G, m_offsets, row_index, total_m, a_rows, N, K, a_q, a_s, b_q, b_s,
+                               y, y_dtype, ld_y, stream=None) -> int:
+    return load().nvfp4_fp8_grouped_gemm(G, m_offsets, row_index, total_m, a_rows, N, K, a_q, a_s,
+                                         b_q, b_s, y, y_dtype, ld_y, _stream(stream))
+
+
+def nvfp4_fp8_grouped_wgrad_raw(G, m_offsets, total_m, N, K, a_q, a_s, b_q, b_s, dw, dw_dtype, flags,
+                                stream=None) -> int:
+    return load().nvfp4_fp8_grouped_wgrad(G, m_offsets, total_m, N, K, a_q, a_s, b_q, b_s, dw,
+                                          dw_dtype, flags, _stream(stream))
+
+
+def _fp8_buffers(layout: str, out, rows_shape, s_shape, cols_shape, st_shape, device, dev: int):
+    """The operands a quantiser writes, new or the caller's (checked):
+    {"rows": Fp8Packed, "cols": Fp8Packed} of the layouts asked for."""
+    _need(layout in ("rows", "cols", "both"), "layout: 'rows', 'cols' or 'both'")
+    names = ("rows", "cols") if layout == "both" else (layout,)
+    given = None if out is None else (tuple(out) if layout == "both" else (out,))
+    _need(given is None or len(given) == len(names), "out: one operand per layout")
+    res = {}
+    for i, n in enumerate(names):
+        q_shape, sc_shape = (rows_shape, s_shape) if n == "rows" else (cols_shape, st_shape)
+        if given is None:
+            res[n] = Fp8Packed((torch.empty(q_shape, dtype=_F8, device=device),
+                                torch.empty(sc_shape, dtype=torch.float32, device=device)))
+        else:
+            o = _fp8(given[i])
+            _need(tuple(o[0].shape) == q_shape and tuple(o[1].shape) == sc_shape and o.dev == dev,
+                  f"out: expected q {q_shape} and s {sc_shape} on x's GPU")
+            res[n] = o
+    return res
+
+
+def _fp8_ptrs(res):
+    return [None if n not in res else _ptr(t) for n in ("rows", "cols") for t in res.get(n, (None, None))]
+
+
+def _fp8_result(layout: str, res):
+    return (res["rows"], res["cols"]) if layout == "both" else res[layout]
+
+
+def nvfp4_fp8_quantize(x: torch.Tensor, block_rows: int = 1, layout: str = "rows", out=None,
+                       stream=None):
+    """x [rows, cols] or [G, rows, cols], fp32/bf16 on the GPU (cols % 16 == 0)
+    -> Fp8Packed.  layout "rows": blocks along the rows, q [.., rows, cols];
+    "cols": the transposed operand, blocks along the columns, q
+    [.., cols, rows rounded up to 16]; "both": the two from one read, as a
+    pair.  block_rows 1 scales 1 x 128 blocks, 128 scales 128 x 128 blocks
+    (weights).  ``out`` reuses buffers."""
+    _need(x.dim() in (2, 3) and x.dtype in _DT_IN, "x: 2-D or 3-D, fp32 or bf16")
+    _need(x.is_cuda, "x: must be on a GPU")
+    _need(block_rows in (1, 128), "block_rows: 1 or 128")
+    lead, (rows, cols) = tuple(x.shape[:-2]), x.shape[-2:]
+    batch = lead[0] if lead else 1
+    _need(cols % 16 == 0, "x: columns must be a multiple of 16")
+    ld = _stride(x, cols, "x")
+    _need(batch <= 1 or x.stride(0) == rows * ld, "x: matrices must follow each other")
+    dev = x.get_device()
+    rows_t = -(-rows // 16) * 16
+    with _on_gpu(dev), _on_stream(stream, dev):
+        res = _fp8_buffers(layout, out, (*lead, rows, cols), (*lead, -(-cols // 128), -(-rows // block_rows)),
+                           (*lead, cols, rows_t),
+                           (*lead, -(-rows_t // 128), cols if block_rows == 1 else -(-cols // 128)),
+                           x.device, dev)
+        st = nvfp4_fp8_quantize_raw(_ptr(x), _DT_IN[x.dtype], batch, rows, cols, ld, block_rows,
+                                    *_fp8_ptrs(res), _stream(None, dev))
+    _check("nvfp4_fp8_quantize", st)
+    return _fp8_result(layout, res)
+
+
+def _groups(m_offsets, dev: int, G: int | None = None) -> int:
+    _need(m_offsets.dtype == torch.int32 and m_offsets.dim() == 1 and m_offsets.numel() >= 1
+          and m_offsets.is_contiguous(), "m_offsets: G + 1 contiguous int32")
+    _need(G is None or m_offsets.numel() == G + 1, "m_offsets: G + 1 contiguous int32")
+    _on_dev(m_offsets, dev, "m_offsets")
+    return m_offsets.numel() - 1
+
+
+def _row_index(row_index, total_m: int, dev: int):
+    if row_index is not None:
+        _need(row_index.dtype == torch.int32 and row_index.numel() == total_m
+              and row_index.is_contiguous(), "row_index: total_m contiguous int32")
+        _on_dev(row_index, dev, "row_index")
+
+
+def nvfp4_fp8_grouped_quantize(x: torch.Tensor, m_offsets: torch.Tensor, layout: str = "cols",
+                               row_index: torch.Tensor | None = None, out=None, stream=None):
+    """Rows sorted by group (m_offsets int32 [G+1], GPU) -> Fp8Packed with 1 x
+    128 blocks.  layout "cols": the transposed operand [cols, P] of
+    nvfp4_fp8_grouped_wgrad, each group's tokens starting at a multiple of
+    128 (P = nvfp4_fp8_grouped_columns(total_m, G)); "rows": q [total_m, cols]
+    (rows of no group stay as they were); "both" as a pair.  With row_index
+    (int32 [total_m], GPU), grouped row r is x[row_index[r]]."""
+    _need(x.dim() == 2 and x.dtype in _DT_IN, "x: 2-D fp32 or bf16")
+    _need(x.is_cuda, "x: must be on a GPU")
+    x_rows, cols = x.shape
+    _need(cols % 16 == 0, "x: columns must be a multiple of 16")
+    ld, dev = _stride(x, cols, "x"), x.get_device()
+    G = _groups(m_offsets, dev)
+    total = x_rows if row_index is None else row_index.numel()
+    _row_index(row_index, total, dev)
+    _need(G > 0 or total == 0, "m_offsets: no groups for the rows")
+    P = nvfp4_fp8_grouped_columns(total, G)
+    with _on_gpu(dev), _on_stream(stream, dev):
+        res = _fp8_buffers(layout, out, (total, cols), (-(-cols // 128), total), (cols, P),
+                           (P // 128, cols), x.device, dev)
+        st = nvfp4_fp8_grouped_quantize_raw(_ptr(x), _DT_IN[x.dtype], G, _ptr(m_offsets),
+                                            None if row_index is None else _ptr(row_index), total,
+                                            x_rows, cols, ld, *_fp8_ptrs(res), _stream(None, dev))
+    _check("nvfp4_fp8_grouped_quantize", st)
+    return _fp8_result(layout, res)
+
+
+def _fp8_out(y, shape, out_dtype: str, accumulate: bool, device, dev: int):
+    """The output (new, or the caller's, checked), its dtype code and row stride."""
+    _need(out_dtype in _DT_OUT, f"out_dtype: one of {sorted(_DT_OUT)}")
+    code, tdt = _DT_OUT[out_dtype]
+    _need(not accumulate or (y is not None and out_dtype == "f32"),
+          "accumulate: needs an fp32 output to add to")
+    if y is None:
+        y = torch.empty(shape, dtype=tdt, device=device)
+    _need(y.dtype == tdt, f"y: dtype {y.dtype}, expected {tdt}")
+    _need(tuple(y.shape) == tuple(shape), f"y: shape {tuple(y.shape)}, expected {tuple(shape)}")
+    _on_dev(y, dev, "y")
+    return y, code, _stride(y, shape[-1], "y")
+
+
+def nvfp4_fp8_gemm(a, b, out_dtype: str = "bf16", y: torch.Tensor | None = None,
+                   accumulate: bool = False, stream=None):
+    """a = Fp8Packed [M, K] with block_rows 1; b = Fp8Packed [N, K] with
+    block_rows 1 or 128 -> y [M, N] = a . b^T.  With accumulate the product
+    is added to the fp32 ``y``.  A linear layer y = x W^T takes x (layout
+    "rows") and W (block_rows 128, "rows"); its input gradient takes dy
+    ("rows") and W ("cols"); its weight gradient dy ("cols") and x ("cols")."""
+    a, b = _fp8(a), _fp8(b)
+    _need(not a.lead and not b.lead and a.K == b.K and a.dev == b.dev,
+          "a and b: 2-D operands with the same K on one GPU")
+    _need(a.block_rows == 1, "a: must have block_rows 1")
+    M, N, K, dev = a.rows, b.rows, a.K, a.dev
+    with _on_gpu(dev), _on_stream(stream, dev):
+        y, code, ld = _fp8_out(y, (M, N), out_dtype, accumulate, a[0].device, dev)
+        st = nvfp4_fp8_gemm_raw(M, N, K, _ptr(a[0]), _ptr(a[1]), _ptr(b[0]), _ptr(b[1]), b.block_rows,
+                                _ptr(y), code, ld, NVFP4_ACCUMULATE if accumulate else 0,
+                                _stream(None, dev))
+    _check("nvfp4_fp8_gemm", st)
+    return y
+
+
+def nvfp4_fp8_grouped_gemm(m_offsets: torch.Tensor, total_m: int, a, b, out_dtype: str = "bf16",
+                           y: torch.Tensor | None = None, stream=None,
+                           row_index: torch.Tensor | None = None):
+    """m_offsets int32 [G+1] (GPU); a = Fp8Packed [total_m, K] (block_rows 1);
+    b = Fp8Packed [G, N, K] with block_rows 128 -> y [total_m, N].  With
+    row_index (int32 [total_m], GPU), grouped row r reads row row_index[r] of
+    a [a_rows, K].  Rows of y of no group stay as they were."""
+    a, b = _fp8(a), _fp8(b)
+    _need(len(b.lead) == 1 and not a.lead and a.K == b.K and a.dev == b.dev,
+          "b: [G, N, K] experts and a: [rows, K] with the same K, on one GPU")
+    _need(a.block_rows == 1, "a: must have block_rows 1")
+    _need(b[1].shape[-1] == -(-b.rows // 128), "b: must have block_rows 128")
+    _need(row_index is not None or a.rows == total_m, "a: total_m rows (or give row_index)")
+    dev = b.dev
+    G = _groups(m_offsets, dev, b.lead[0])
+    _row_index(row_index, total_m, dev)
+    with _on_gpu(dev), _on_stream(stream, dev):
+        y, code, ld = _fp8_out(y, (total_m, b.rows), out_dtype, False, b[0].device, dev)
+        st = nvfp4_fp8_grouped_gemm_raw(G, _ptr(m_offsets),
+                                        None if row_index is None else _ptr(row_index), total_m,
+                                        a.rows, b.rows, b.K, _ptr(a[0]), _ptr(a[1]), _ptr(b[0]),
+                                        _ptr(b[1]), _ptr(y), code, ld, _stream(None, dev))
+    _check("nvfp4_fp8_grouped_gemm", st)
+    return y
+
+
+def nvfp4_fp8_grouped_wgrad(m_offsets: torch.Tensor, total_m: int, a, b, out_dtype: str = "f32",
+                            dw: torch.Tensor | None = None, accumulate: bool = False, stream=None):
+    """Experts' weight gradients dw [G, N, K] from the transposed operands of
+    nvfp4_fp8_grouped_quantize: a = dy [N, P], b = x [K, P].  With accumulate
+    they are added to the fp32 ``dw``."""
+    a, b = _fp8(a), _fp8(b)
+    _need(not a.lead and not b.lead and a.K == b.K and a.dev == b.dev,
+          "a and b: 2-D transposed operands with the same columns on one GPU")
+    _need(a.block_rows == 1 and b.block_rows == 1, "a and b: must have block_rows 1")
+    dev = a.dev
+    G = _groups(m_offsets, dev)
+    _need(a.K == nvfp4_fp8_grouped_columns(total_m, G),
+          f"a and b: {a.K} columns, expected nvfp4_fp8_grouped_columns({total_m}, {G})")
+    _need(G > 0 or total_m == 0, "m_offsets: no groups for the rows")
+    with _on_gpu(dev), _on_stream(stream, dev):
+        dw, code, ld = _fp8_out(dw, (G, a.rows, b.rows), out_dtype, accumulate, a[0].device, dev)
+        _need(dw.is_contiguous(), "dw: must be contiguous")
+        st = nvfp4_fp8_grouped_wgrad_raw(G, _ptr(m_offsets), total_m, a.rows, b.rows, _ptr(a[0]),
+                                         _ptr(a[1]), _ptr(b[0]), _ptr(b[1]), _ptr(dw), code,
+                                         NVFP4_ACCUMULATE if accumulate else 0, _stream(None, dev))
+    _check("nvfp4_fp8_grouped_wgrad", st)
+    return dw
+
+
+# --------------------------------------------------------------------------
+# expert router: top-k, counts and order, balance loss, and their gradient
+# --------------------------------------------------------------------------
+
+class MoeRoute(typing.NamedTuple):
+    """What nvfp4_moe_route writes (include/nvfp4.h has each one's meaning)."""
+    expert_index: torch.Tensor   # int32 [T, topk]
+    weights: torch.Tensor        # fp32 [T, topk]
+    counts: torch.Tensor         # int32 [E]
+    m_offsets: torch.Tensor      # int32 [E + 1]
+    row_index: torch.Tensor      # int32 [T * topk]
+    pair_row: torch.Tensor       # int32 [T, topk]
+    routed: torch.Tensor         # int32 [1]
+    loss: torch.Tensor           # fp32 [1]
+
+
+def nvfp4_moe_route_workspace_bytes(T: int, E: int) -> int:
+    return int(load().nvfp4_moe_route_workspace_bytes(T, E))
+
+
+def nvfp4_moe_route_raw(T, E, topk, logits, logits_dtype, ld_logits, token_mask, flags,
+                        expert_index, weights, counts, m_offsets, row_index, pair_row, routed, loss,
+                        workspace, workspace_bytes, stream=None) -> int:
+    return load().nvfp4_moe_route(T, E, topk, logits, logits_dtype, ld_logits, token_mask, flags,
+                                  expert_index, weights, counts, m_offsets, row_index, pair_row,
+                                  routed, loss, workspace, workspace_bytes, _stream(stream))
+
+
+def nvfp4_moe_route_backward_raw(T, E, topk, logits, logits_dtype, ld_logits, token_mask, flags,
+                                 expert_index, counts, routed, d_weights, d_loss, d_logits, ld_d,
+                                 stream=None) -> int:
+    return load().nvfp4_moe_route_backward(T, E, topk, logits, logits_dtype, ld_logits, token_mask,
+                                           flags, expert_index, counts, routed, d_weights, d_loss,
+                                           d_logits, ld_d, _stream(stream))
+
+
+def _logits(logits, mask):
+    _need(logits.dim() == 2 and logits.dtype in _DT_IN, "logits: 2-D fp32 or bf16")
+    _need(logits.is_cuda, "logits: must be on a GPU")
+    T, E = logits.shape
+    _need(E >= 1, "logits: at least one expert")
+    dev = logits.get_device()
+    if mask is not None:
+        _need(mask.dtype in (torch.bool, torch.uint8) and tuple(mask.shape) == (T,)
+              and mask.is_contiguous(), "mask: T contiguous bool or uint8")
+        _on_dev(mask, dev, "mask")
+    return T, E, _stride(logits, E, "logits"), dev
+
+
+def nvfp4_moe_route(logits: torch.Tensor, topk: int, mask: torch.Tensor | None = None,
+                    renormalize: bool = False, workspace: torch.Tensor | None = None,
+                    stream=None) -> MoeRoute:
+    """logits [T, E] fp32/bf16 (GPU) -> MoeRoute: each token's topk experts and
+    weights, the expert-sorted order the grouped GEMMs take (m_offsets,
+    row_index, with pair_row the row of each choice), the per-expert counts
+    and the balance loss.  ``mask`` [T]: tokens at 0 are not routed.
+    ``renormalize``: weights are the softmax over the chosen experts."""
+    T, E, ld, dev = _logits(logits, mask)
+    n = T * topk
+    _need(1 <= topk <= E, f"topk: 1 to {E}")
+    need = nvfp4_moe_route_workspace_bytes(T, E)
+    if workspace is not None:
+        _on_dev(workspace, dev, "workspace")
+        _need(workspace.is_contiguous(), "workspace: must be contiguous")
+    with _on_gpu(dev), _on_stream(stream, dev):
+        # one allocation for the outputs; a tail of it is the workspace
+        own = 0 if workspace is not None else -(-need // 4)
+        buf = torch.empty(4 * n + 2 * E + 3 + own, dtype=torch.int32, device=logits.device)
+        ei, w, ri, pr, counts, off, routed, loss, ws = buf.split_with_sizes((n, n, n, n, E, E + 1, 1, 1, own))
+        r = MoeRoute(ei.view(T, topk), w.view(torch.float32).view(T, topk), counts, off, ri,
+                     pr.view(T, topk), routed, loss.view(torch.float32))
+        ws = ws if workspace is None else workspace
+        st = nvfp4_moe_route_raw(T, E, topk, _ptr(logits), _DT_IN[logits.dtype], ld,
+                                 None if mask is None else _ptr(mask),
+                                 NVFP4_ROUTE_RENORMALIZE if renormalize else 0,
+                                 _ptr(r.expert_index), _ptr(r.weights), _ptr(counts), _ptr(off),
+                                 _ptr(ri), _ptr(r.pair_row), _ptr(routed), _ptr(r.loss), _ptr(ws),
+                                 ws.numel() * ws.element_size(), _stream(None, dev))
+    _check("nvfp4_moe_route", st)
+    return r
+
+
+def nvfp4_moe_route_backward(logits: torch.Tensor, route: MoeRoute,
+                             d_weights: torch.Tensor | None = None,
+                             d_loss: torch.Tensor | None = None, mask: torch.Tensor | None = None,
+                             renormalize: bool = False, out: torch.Tensor | None = None, stream=None):
+    """Gradient of the logits from d_weights fp32 [T, topk] and d_loss (one
+    fp32 value, GPU), given what nvfp4_moe_route returned for them and the
+    same mask and renormalize; ``out`` reuses a buffer of the logits' shape."""
+    T, E, ld, dev = _logits(logits, mask)
+    e = route.expert_index
+    _need(e.dim() == 2 and e.shape[0] == T and e.dtype == torch.int32 and e.is_contiguous()
+          and route.counts.dtype == torch.int32 and route.counts.numel() == E
+          and route.counts.is_contiguous() and route.routed.dtype == torch.int32
+          and route.routed.numel() == 1, "route: not nvfp4_moe_route's answer for these logits")
+    for t in (e, route.counts, route.routed):
+        _on_dev(t, dev, "route")
+    topk = e.shape[1]
+    if d_weights is not None:
+        _need(d_weights.dtype == torch.float32 and tuple(d_weights.shape) == (T, topk)
+              and d_weights.is_contiguous(), "d_weights: contiguous fp32 [T, topk]")
+        _on_dev(d_weights, dev, "d_weights")
+    if d_loss is not None:
+        _need(d_loss.dtype == torch.float32 and d_loss.numel() == 1, "d_loss: one fp32 value")
+        _on_dev(d_loss, dev, "d_loss")
+    with _on_gpu(dev), _on_stream(stream, dev):
+        if out is None:
+            out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+        _need(out.dtype == logits.dtype and tuple(out.shape) == (T, E), "out: the logits' dtype and shape")
+        _on_dev(out, dev, "out")
+        st = nvfp4_moe_route_backward_raw(T, E, topk, _ptr(logits), _DT_IN[logits.dtype], ld,
+                                          None if mask is None else _ptr(mask),
+                                          NVFP4_ROUTE_RENORMALIZE if renormalize else 0, _ptr(e),
+                                          _ptr(route.counts), _ptr(route.routed),
+                                          None if d_weights is None else _ptr(d_weights),
+                                          None if d_loss is None else _ptr(d_loss), _ptr(out),
+                                          _stride(out, E, "out"), _stream(None, dev))
+    _check("nvfp4_moe_route_backward", st)
+    return out

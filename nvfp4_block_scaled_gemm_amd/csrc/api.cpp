@@ -103,6 +103,62 @@ int gemm_dispatch(int64_t M, int64_t N, int64_t K, const uint8_t* a_q, const uin
   }
 }
 
+// ---- FP8 block-128 operators ----------------------------------------------
+
+constexpr int64_t kMaxFp8K = (int64_t)1 << 22;  // 256 rows of K bytes stay below 2^31
+
+bool dtype_ok(int dt) { return dt == NVFP4_F32 || dt == NVFP4_BF16; }
+int64_t dtype_size(int dt) { return dt == NVFP4_F32 ? 4 : 2; }
+
+// Checks both quantisers share; NVFP4_OK, an error, or 1: nothing to do.
+int fp8_quantize_check(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ld_x,
+                       const uint8_t* q, const float* s, const uint8_t* qt, const float* st) {
+  if (rows < 0 || cols < 0 || cols % 16 != 0) return NVFP4_ERR_INVALID_ARG;
+  if (!dtype_ok(x_dtype)) return NVFP4_ERR_INVALID_ARG;
+  if (rows > kMaxDim || cols > kMaxDim || ld_x > (kMaxDim << 1)) return NVFP4_ERR_UNSUPPORTED;
+  if (rows == 0 || cols == 0) return 1;
+  if (x == nullptr || ld_x < cols) return NVFP4_ERR_INVALID_ARG;
+  if ((q == nullptr) != (s == nullptr) || (qt == nullptr) != (st == nullptr))
+    return NVFP4_ERR_INVALID_ARG;
+  if (q == nullptr && qt == nullptr) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || (ld_x * dtype_size(x_dtype)) % 16 != 0) return NVFP4_ERR_UNSUPPORTED;
+  if (!aligned(q, 16) || !aligned(qt, 16) || !aligned(s, 4) || !aligned(st, 4))
+    return NVFP4_ERR_UNSUPPORTED;
+  return NVFP4_OK;
+}
+
+// Output of an FP8 product and its flags.
+int fp8_out_check(const void* y, int y_dtype, int64_t N, int64_t ld_y, unsigned flags) {
+  if (!dtype_ok(y_dtype) || (flags & ~NVFP4_ACCUMULATE)) return NVFP4_ERR_INVALID_ARG;
+  if ((flags & NVFP4_ACCUMULATE) && y_dtype != NVFP4_F32) return NVFP4_ERR_INVALID_ARG;
+  if (y == nullptr || ld_y < N) return NVFP4_ERR_INVALID_ARG;
+  if (ld_y > (kMaxDim << 1)) return NVFP4_ERR_UNSUPPORTED;
+  return aligned(y, dtype_size(y_dtype)) ? NVFP4_OK : NVFP4_ERR_UNSUPPORTED;
+}
+
+nvfp4::Fp8Out fp8_out(void* y, int y_dtype, int64_t ld_y, unsigned flags) {
+  const bool vec = aligned(y, 16) && (ld_y * dtype_size(y_dtype)) % 16 == 0;
+  return {y, ld_y, y_dtype, (flags & NVFP4_ACCUMULATE) != 0, vec};
+}
+
+int fp8_operands_check(const uint8_t* a_q, const float* a_s, const uint8_t* b_q,
+                       const float* b_s) {
+  if (a_q == nullptr || a_s == nullptr || b_q == nullptr || b_s == nullptr)
+    return NVFP4_ERR_INVALID_ARG;
+  return aligned(a_q, 16) && aligned(b_q, 16) && aligned(a_s, 4) && aligned(b_s, 4)
+             ? NVFP4_OK
+             : NVFP4_ERR_UNSUPPORTED;
+}
+
+// Checks both router calls share.
+int route_check(int64_t T, int64_t E, int32_t topk, int dtype, int64_t ld, unsigned flags) {
+  if (T < 0 || E < 1 || topk < 1 || topk > E || !dtype_ok(dtype)) return NVFP4_ERR_INVALID_ARG;
+  if (flags & ~NVFP4_ROUTE_RENORMALIZE) return NVFP4_ERR_INVALID_ARG;
+  if (E > 1024 || topk > 16 || T > kMaxDim || T * topk >= ((int64_t)1 << 31))
+    return NVFP4_ERR_UNSUPPORTED;
+  return T > 0 && ld < E ? NVFP4_ERR_INVALID_ARG : NVFP4_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -294,6 +350,146 @@ int nvfp4_mxfp4_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a_q, const 
                                                st));
   return from_hip(nvfp4::launch_mx_gemm_generic(M, N, K, a_q, a_s, b_q, b_s, y, (int)y_dtype,
                                                 ld_y, st));
+}
+
+int nvfp4_fp8_quantize(const void* x, nvfp4_dtype x_dtype, int64_t batch, int64_t rows,
+                       int64_t cols, int64_t ld_x, int block_rows, uint8_t* q, float* s,
+                       uint8_t* qt, float* st, void* stream) {
+  if (batch < 0 || (block_rows != 1 && block_rows != 128)) return NVFP4_ERR_INVALID_ARG;
+  if (batch > kMaxDim) return NVFP4_ERR_UNSUPPORTED;
+  if (batch == 0) rows = 0;
+  const int v = fp8_quantize_check(x, (int)x_dtype, rows, cols, ld_x, q, s, qt, st);
+  if (v != NVFP4_OK) return v == 1 ? NVFP4_OK : v;
+  return from_hip(nvfp4::launch_fp8_quantize(x, (int)x_dtype, batch, rows, cols, ld_x, block_rows,
+                                             q, s, qt, st, (hipStream_t)stream));
+}
+
+int64_t nvfp4_fp8_grouped_columns(int64_t total_m, int32_t G) {
+  if (total_m <= 0 || G <= 0) return 0;
+  return nvfp4::fp8_padded_tokens(total_m, G);
+}
+
+int nvfp4_fp8_grouped_quantize(const void* x, nvfp4_dtype x_dtype, int32_t G,
+                               const int32_t* m_offsets, const int32_t* row_index,
+                               int64_t total_m, int64_t x_rows, int64_t cols, int64_t ld_x,
+                               uint8_t* q, float* s, uint8_t* qt, float* st, void* stream) {
+  if (G < 0 || (G == 0 && total_m != 0)) return NVFP4_ERR_INVALID_ARG;
+  if (row_index != nullptr && x_rows < 0) return NVFP4_ERR_INVALID_ARG;
+  if (row_index != nullptr && x_rows > kMaxDim) return NVFP4_ERR_UNSUPPORTED;
+  const int v = fp8_quantize_check(x, (int)x_dtype, total_m, cols, ld_x, q, s, qt, st);
+  if (v != NVFP4_OK) return v == 1 ? NVFP4_OK : v;
+  if (m_offsets == nullptr) return NVFP4_ERR_INVALID_ARG;
+  return from_hip(nvfp4::launch_fp8_grouped_quantize(x, (int)x_dtype, G, m_offsets, row_index,
+                                                     total_m, x_rows, cols, ld_x, q, s, qt, st,
+                                                     (hipStream_t)stream));
+}
+
+int nvfp4_fp8_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a_q, const float* a_s,
+                   const uint8_t* b_q, const float* b_s, int b_block_rows, void* y,
+                   nvfp4_dtype y_dtype, int64_t ld_y, unsigned flags, void* stream) {
+  if (M < 0 || N < 0 || K < 0 || K % 16 != 0) return NVFP4_ERR_INVALID_ARG;
+  if (b_block_rows != 1 && b_block_rows != 128) return NVFP4_ERR_INVALID_ARG;
+  if (M > kMaxDim || N > kMaxDim || K > kMaxFp8K) return NVFP4_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return NVFP4_OK;
+  int v = fp8_out_check(y, (int)y_dtype, N, ld_y, flags);
+  if (v == NVFP4_OK && K > 0) v = fp8_operands_check(a_q, a_s, b_q, b_s);
+  if (v != NVFP4_OK) return v;
+  return from_hip(nvfp4::launch_fp8_gemm(M, N, K, {a_q, a_s}, {b_q, b_s}, b_block_rows,
+                                         fp8_out(y, (int)y_dtype, ld_y, flags),
+                                         (hipStream_t)stream));
+}
+
+int nvfp4_fp8_grouped_gemm(int32_t G, const int32_t* m_offsets, const int32_t* row_index,
+                           int64_t total_m, int64_t a_rows, int64_t N, int64_t K,
+                           const uint8_t* a_q, const float* a_s, const uint8_t* b_q,
+                           const float* b_s, void* y, nvfp4_dtype y_dtype, int64_t ld_y,
+                           void* stream) {
+  if (G < 0 || total_m < 0 || N < 0 || K < 0 || K % 16 != 0) return NVFP4_ERR_INVALID_ARG;
+  if ((G == 0 && total_m != 0) || a_rows < 0) return NVFP4_ERR_INVALID_ARG;
+  if (row_index == nullptr && a_rows != 0 && a_rows != total_m) return NVFP4_ERR_INVALID_ARG;
+  if (total_m > kMaxDim || a_rows > kMaxDim || N > kMaxDim || K > kMaxFp8K)
+    return NVFP4_ERR_UNSUPPORTED;
+  if (total_m == 0 || N == 0) return NVFP4_OK;
+  if (m_offsets == nullptr) return NVFP4_ERR_INVALID_ARG;
+  int v = fp8_out_check(y, (int)y_dtype, N, ld_y, 0);
+  if (v == NVFP4_OK && K > 0) v = fp8_operands_check(a_q, a_s, b_q, b_s);
+  if (v != NVFP4_OK) return v;
+  if (row_index != nullptr && a_rows * K >= ((int64_t)1 << 31)) return NVFP4_ERR_UNSUPPORTED;
+  return from_hip(nvfp4::launch_fp8_grouped(G, m_offsets, row_index, total_m, a_rows, N, K,
+                                            {a_q, a_s}, {b_q, b_s},
+                                            fp8_out(y, (int)y_dtype, ld_y, 0),
+                                            (hipStream_t)stream));
+}
+
+int nvfp4_fp8_grouped_wgrad(int32_t G, const int32_t* m_offsets, int64_t total_m, int64_t N,
+                            int64_t K, const uint8_t* a_q, const float* a_s, const uint8_t* b_q,
+                            const float* b_s, void* dw, nvfp4_dtype dw_dtype, unsigned flags,
+                            void* stream) {
+  if (G < 0 || total_m < 0 || N < 0 || K < 0) return NVFP4_ERR_INVALID_ARG;
+  if (G == 0 && total_m != 0) return NVFP4_ERR_INVALID_ARG;
+  if (total_m > kMaxDim || N > kMaxDim || K > kMaxDim) return NVFP4_ERR_UNSUPPORTED;
+  if (G == 0 || N == 0 || K == 0) return NVFP4_OK;
+  const int64_t P = nvfp4_fp8_grouped_columns(total_m, G);
+  if (P > kMaxFp8K) return NVFP4_ERR_UNSUPPORTED;
+  if (m_offsets == nullptr) return NVFP4_ERR_INVALID_ARG;
+  int v = fp8_out_check(dw, (int)dw_dtype, K, K, flags);
+  if (v == NVFP4_OK && P > 0) v = fp8_operands_check(a_q, a_s, b_q, b_s);
+  if (v != NVFP4_OK) return v;
+  return from_hip(nvfp4::launch_fp8_wgrad(G, m_offsets, total_m, P, N, K, {a_q, a_s}, {b_q, b_s},
+                                          fp8_out(dw, (int)dw_dtype, K, flags),
+                                          (hipStream_t)stream));
+}
+
+size_t nvfp4_moe_route_workspace_bytes(int64_t T, int64_t E) {
+  if (T < 0 || E < 1) return 0;
+  return nvfp4::moe_route_workspace_bytes(T, E);
+}
+
+int nvfp4_moe_route(int64_t T, int64_t E, int32_t topk, const void* logits,
+                    nvfp4_dtype logits_dtype, int64_t ld_logits, const uint8_t* token_mask,
+                    unsigned flags, int32_t* expert_index, float* weights, int32_t* counts,
+                    int32_t* m_offsets, int32_t* row_index, int32_t* pair_row, int32_t* routed,
+                    float* loss, void* workspace, size_t workspace_bytes, void* stream) {
+  const int v = route_check(T, E, topk, (int)logits_dtype, ld_logits, flags);
+  if (v != NVFP4_OK) return v;
+  if (counts == nullptr || m_offsets == nullptr || routed == nullptr || loss == nullptr ||
+      workspace == nullptr)
+    return NVFP4_ERR_INVALID_ARG;
+  if (T > 0 && (logits == nullptr || expert_index == nullptr || weights == nullptr ||
+                row_index == nullptr || pair_row == nullptr))
+    return NVFP4_ERR_INVALID_ARG;
+  if (workspace_bytes < nvfp4::moe_route_workspace_bytes(T, E)) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned(logits, dtype_size((int)logits_dtype)) || !aligned(expert_index, 4) ||
+      !aligned(weights, 4) || !aligned(counts, 4) || !aligned(m_offsets, 4) ||
+      !aligned(row_index, 4) || !aligned(pair_row, 4) || !aligned(routed, 4) ||
+      !aligned(loss, 4) || !aligned(workspace, 4))
+    return NVFP4_ERR_UNSUPPORTED;
+  const nvfp4::RouteOut out{expert_index, weights, counts, m_offsets, row_index, pair_row, routed, loss};
+  return from_hip(nvfp4::launch_moe_route(T, E, topk, logits, (int)logits_dtype, ld_logits,
+                                          token_mask, (flags & NVFP4_ROUTE_RENORMALIZE) != 0, out,
+                                          workspace, (hipStream_t)stream));
+}
+
+int nvfp4_moe_route_backward(int64_t T, int64_t E, int32_t topk, const void* logits,
+                             nvfp4_dtype logits_dtype, int64_t ld_logits,
+                             const uint8_t* token_mask, unsigned flags,
+                             const int32_t* expert_index, const int32_t* counts,
+                             const int32_t* routed, const float* d_weights, const float* d_loss,
+                             void* d_logits, int64_t ld_d, void* stream) {
+  const int v = route_check(T, E, topk, (int)logits_dtype, ld_logits, flags);
+  if (v != NVFP4_OK) return v;
+  if (T == 0) return NVFP4_OK;
+  if (logits == nullptr || expert_index == nullptr || counts == nullptr || routed == nullptr ||
+      d_logits == nullptr || ld_d < E)
+    return NVFP4_ERR_INVALID_ARG;
+  const uintptr_t es = (uintptr_t)dtype_size((int)logits_dtype);
+  if (!aligned(logits, es) || !aligned(d_logits, es) || !aligned(expert_index, 4) ||
+      !aligned(counts, 4) || !aligned(routed, 4) || !aligned(d_weights, 4) || !aligned(d_loss, 4))
+    return NVFP4_ERR_UNSUPPORTED;
+  return from_hip(nvfp4::launch_moe_route_backward(
+      T, E, topk, logits, (int)logits_dtype, ld_logits, token_mask,
+      (flags & NVFP4_ROUTE_RENORMALIZE) != 0, expert_index, counts, routed, d_weights, d_loss,
+      d_logits, ld_d, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,229 @@
+// FP8 block-128 products: dense, per expert, and the experts' weight
+// gradients.  The tile itself is in fp8_tile.h; here is which tile a
+// workgroup takes.
+#include <atomic>
+
+#include "fp8_tile.h"
+#include "nvfp4_internal.h"
+
+namespace nvfp4 {
+namespace {
+
+using namespace fp8;
+
+constexpr int kXcds = 8;
+
+__device__ __forceinline__ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Hardware workgroup ids go round-robin over the XCDs; a bijection that
+// gives each XCD a run of neighbouring logical ids (shared rows in its L2).
+__device__ __forceinline__ int xcd_run(int pid, int n) {
+  const int per = n / kXcds, extra = n % kXcds;
+  const int x = pid % kXcds, i = pid / kXcds;
+  return x * per + min(x, extra) + i;
+}
+
+// Rows [r0, r0 + rows) of a whole operand as a tile operand.
+__device__ __forceinline__ TileOperand rows_of(const uint8_t* q, const float* s, int64_t s_ld,
+                                               int block_rows, int64_t r0, int rows, int64_t K) {
+  const int ns = block_rows == 1 ? rows : (rows + kBlock - 1) / kBlock;
+  return {q + r0 * K, s + r0 / block_rows, s_ld, (uint32_t)(rows * K), (uint32_t)ns * 4, nullptr, 0, 0};
+}
+
+__device__ __forceinline__ TileOut out_of(const Fp8Out& y, int64_t at, int m, int n) {
+  const int es = y.dtype == 0 ? 4 : 2;
+  return {(uint8_t*)y.y + at * es, y.ld, m, n, y.dtype, y.add, y.vec};
+}
+
+template <int BM, int BN, int WM, int WN, int STAGES, bool BROWS, bool WIDE>
+__global__ __launch_bounds__(64 * WM * WN) void fp8_dense_kernel(int64_t M, int64_t N, int64_t K,
+                                                                 Fp8Operand a, Fp8Operand b,
+                                                                 Fp8Out y) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  const int tiles_m = (int)ceil_div(M, BM), tiles_n = (int)ceil_div(N, BN);
+  // groups of 8 tile rows, walked column by column
+  const int pid = xcd_run(blockIdx.x, gridDim.x);
+  const int group = pid / (8 * tiles_n), first = group * 8, gsz = min(tiles_m - first, 8);
+  const int in = pid - group * 8 * tiles_n;
+  const int64_t m0 = (int64_t)(first + in % gsz) * BM, n0 = (int64_t)(in / gsz) * BN;
+  const int rm = (int)min((int64_t)BM, M - m0), rn = (int)min((int64_t)BN, N - n0);
+  using T = Tile<BM, BN, WM, WN, STAGES, BROWS, WIDE>;
+  T::template run<false>(rows_of(a.q, a.s, M, 1, m0, rm, K),
+                         rows_of(b.q, b.s, BROWS ? N : ceil_div(N, kBlock), BROWS ? 1 : kBlock, n0, rn, K),
+                         (uint32_t)K, (uint32_t)K, out_of(y, m0 * y.ld + n0, rm, rn), smem);
+}
+
+// Experts' products: workgroups walk the list of (expert, tile column, tile
+// row) tiles, tile rows fastest so that neighbours share a weight tile.  The
+// list is known on the device only: each wave keeps 64 experts' running tile
+// counts in its lanes and finds a tile's expert by one ballot.
+template <int BM, int BN, int WM, int WN, int STAGES, bool GATHER, bool WIDE>
+__global__ __launch_bounds__(64 * WM * WN) void fp8_grouped_kernel(
+    int G, const int32_t* __restrict__ offsets, const int32_t* __restrict__ row_index,
+    int64_t total_m, int64_t a_rows, int64_t N, int64_t K, Fp8Operand a, Fp8Operand b, Fp8Out y) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  using T = Tile<BM, BN, WM, WN, STAGES, false, WIDE>;
+  const int lane = threadIdx.x & 63;
+  const int64_t tiles_n = ceil_div(N, BN), nb = ceil_div(N, kBlock), kb = ceil_div(K, kBlock);
+  const int step = gridDim.x;
+  int64_t before = 0;            // tile rows of the experts below e0
+  int e0 = 0;
+  auto load = [&](Segment& sg) {
+    sg = e0 + lane < G ? segment(offsets, e0 + lane, total_m) : Segment{0, 0};
+    return wave_scan((uint32_t)((sg.n + BM - 1) / BM));
+  };
+  Segment sg;
+  uint32_t upto = load(sg);
+  for (int64_t u = xcd_run(blockIdx.x, step);; u += step) {
+    uint32_t all = __builtin_amdgcn_readlane(upto, 63);
+    while (u >= (before + all) * tiles_n) {
+      before += all;
+      e0 += 64;
+      if (e0 >= G) return;
+      upto = load(sg);
+      all = __builtin_amdgcn_readlane(upto, 63);
+    }
+    // first lane whose running count passes the tile
+    const int64_t v = u - before * tiles_n;
+    const uint64_t past = __ballot((int64_t)upto * tiles_n > v);
+    const int l = __builtin_ctzll(past);
+    const int64_t start = l == 0 ? 0 : (int64_t)__builtin_amdgcn_readlane(upto, l - 1);
+    const int32_t lo = __builtin_amdgcn_readlane(sg.lo, l), n = __builtin_amdgcn_readlane(sg.n, l);
+    const int32_t te = (n + BM - 1) / BM;
+    const int32_t w = (int32_t)(v - start * tiles_n);
+    const int32_t tm = w % te, tn = w / te;
+    const int64_t e = e0 + l, m0 = lo + (int64_t)tm * BM, n0 = (int64_t)tn * BN;
+    const int rm = min(BM, n - tm * BM), rn = (int)min((int64_t)BN, N - n0);
+    TileOperand A;
+    if constexpr (GATHER)
+      A = {a.q, a.s, a_rows, (uint32_t)(a_rows * K), (uint32_t)a_rows * 4, row_index + m0, rm, (int32_t)a_rows};
+    else
+      A = rows_of(a.q, a.s, total_m, 1, m0, rm, K);
+    const TileOperand B = rows_of(b.q + e * N * K, b.s + e * kb * nb, nb, kBlock, n0, rn, K);
+    T::template run<GATHER>(A, B, (uint32_t)K, (uint32_t)K, out_of(y, m0 * y.ld + n0, rm, rn), smem);
+    workgroup_barrier();  // every wave is past its last fragment reads
+  }
+}
+
+// dW_e = A_e . B_e^T over the expert's own columns of the transposed
+// operands; each expert's columns start on a block border.
+template <int BM, int BN, int WM, int WN, int STAGES, bool WIDE>
+__global__ __launch_bounds__(64 * WM * WN) void fp8_wgrad_kernel(
+    int G, const int32_t* __restrict__ offsets, int64_t total_m, int64_t P, int64_t N, int64_t K,
+    Fp8Operand a, Fp8Operand b, Fp8Out y) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  using T = Tile<BM, BN, WM, WN, STAGES, true, WIDE>;
+  const int tiles_m = (int)ceil_div(N, BM), tiles_n = (int)ceil_div(K, BN);
+  const int pid = xcd_run(blockIdx.x, gridDim.x);
+  const int e = pid / (tiles_m * tiles_n), in = pid % (tiles_m * tiles_n);
+  const int64_t m0 = (int64_t)(in % tiles_m) * BM, n0 = (int64_t)(in / tiles_m) * BN;
+  const int lane = threadIdx.x & 63;
+  uint32_t blocks = 0;  // blocks of the experts before e
+  for (int i = lane; i < e; i += 64) blocks += (uint32_t)((segment(offsets, i, total_m).n + kBlock - 1) / kBlock);
+  blocks = __builtin_amdgcn_readlane(wave_scan(blocks), 63);
+  const int64_t k0 = min((int64_t)blocks * kBlock, P);
+  const int32_t cnt = __builtin_amdgcn_readfirstlane(segment(offsets, e, total_m).n);
+  const int64_t len = min(ceil_div(cnt, kBlock) * kBlock, P - k0);
+  const int rm = (int)min((int64_t)BM, N - m0), rn = (int)min((int64_t)BN, K - n0);
+  const int64_t b0 = k0 / kBlock;
+  // rows are P bytes apart: the range ends with the tile's last row
+  TileOperand A{a.q + m0 * P + k0, a.s + b0 * N + m0, N, (uint32_t)(rm * P - k0), (uint32_t)rm * 4, nullptr, 0, 0};
+  TileOperand B{b.q + n0 * P + k0, b.s + b0 * K + n0, K, (uint32_t)(rn * P - k0), (uint32_t)rn * 4, nullptr, 0, 0};
+  T::template run<false>(A, B, (uint32_t)len, (uint32_t)P, out_of(y, ((int64_t)e * N + m0) * K + n0, rm, rn), smem);
+}
+
+// Allows a kernel its LDS, once per kernel and device.
+template <typename Kern>
+hipError_t allow_lds(Kern kern, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_acquire) & bit) return hipSuccess;
+  e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == hipSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
+template <bool BROWS, bool WIDE>
+hipError_t dense(int64_t M, int64_t N, int64_t K, Fp8Operand a, Fp8Operand b, Fp8Out y,
+                 hipStream_t stream) {
+  constexpr int BM = 128, BN = 128, S = 2;
+  using T = Tile<BM, BN, 2, 2, S, BROWS, WIDE>;
+  auto kern = fp8_dense_kernel<BM, BN, 2, 2, S, BROWS, WIDE>;
+  static std::atomic<uint64_t> done{0};
+  const hipError_t err = allow_lds(kern, T::kSmem, done);
+  if (err != hipSuccess) return err;
+  const int64_t tiles = ((M + BM - 1) / BM) * ((N + BN - 1) / BN);
+  if (tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
+  kern<<<(unsigned)tiles, T::kThreads, T::kSmem, stream>>>(M, N, K, a, b, y);
+  return hipGetLastError();
+}
+
+template <bool GATHER, bool WIDE>
+hipError_t grouped(int32_t G, const int32_t* m_offsets, const int32_t* row_index, int64_t total_m,
+                   int64_t a_rows, int64_t N, int64_t K, Fp8Operand a, Fp8Operand b, Fp8Out y,
+                   hipStream_t stream) {
+  constexpr int BM = 64, BN = 128, S = 2;
+  using T = Tile<BM, BN, 2, 2, S, false, WIDE>;
+  auto kern = fp8_grouped_kernel<BM, BN, 2, 2, S, GATHER, WIDE>;
+  static std::atomic<uint64_t> done{0};
+  const hipError_t err = allow_lds(kern, T::kSmem, done);
+  if (err != hipSuccess) return err;
+  kern<<<768, T::kThreads, T::kSmem, stream>>>(G, m_offsets, row_index, total_m, a_rows, N, K, a, b, y);
+  return hipGetLastError();
+}
+
+template <bool WIDE>
+hipError_t wgrad(int32_t G, const int32_t* m_offsets, int64_t total_m, int64_t P, int64_t N,
+                 int64_t K, Fp8Operand a, Fp8Operand b, Fp8Out y, hipStream_t stream) {
+  constexpr int BM = 128, BN = 128, S = 2;
+  using T = Tile<BM, BN, 2, 2, S, true, WIDE>;
+  auto kern = fp8_wgrad_kernel<BM, BN, 2, 2, S, WIDE>;
+  static std::atomic<uint64_t> done{0};
+  const hipError_t err = allow_lds(kern, T::kSmem, done);
+  if (err != hipSuccess) return err;
+  const int64_t tiles = (int64_t)G * ((N + BM - 1) / BM) * ((K + BN - 1) / BN);
+  if (tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
+  kern<<<(unsigned)tiles, T::kThreads, T::kSmem, stream>>>(G, m_offsets, total_m, P, N, K, a, b, y);
+  return hipGetLastError();
+}
+
+// Calls f with the output's width as a constant: fp32 outputs take the wide
+// products, bf16 ones the 8-bit.
+template <typename F>
+hipError_t by_width(const Fp8Out& y, F&& f) {
+  return y.dtype == 0 ? f(std::true_type{}) : f(std::false_type{});
+}
+
+}  // namespace
+
+hipError_t launch_fp8_gemm(int64_t M, int64_t N, int64_t K, Fp8Operand a, Fp8Operand b,
+                           int b_block_rows, Fp8Out y, hipStream_t stream) {
+  return by_width(y, [&](auto wide) {
+    constexpr bool W = decltype(wide)::value;
+    return b_block_rows == 1 ? dense<true, W>(M, N, K, a, b, y, stream)
+                             : dense<false, W>(M, N, K, a, b, y, stream);
+  });
+}
+
+hipError_t launch_fp8_grouped(int32_t G, const int32_t* m_offsets, const int32_t* row_index,
+                              int64_t total_m, int64_t a_rows, int64_t N, int64_t K, Fp8Operand a,
+                              Fp8Operand b, Fp8Out y, hipStream_t stream) {
+  return by_width(y, [&](auto wide) {
+    constexpr bool W = decltype(wide)::value;
+    return row_index != nullptr
+               ? grouped<true, W>(G, m_offsets, row_index, total_m, a_rows, N, K, a, b, y, stream)
+               : grouped<false, W>(G, m_offsets, row_index, total_m, a_rows, N, K, a, b, y, stream);
+  });
+}
+
+hipError_t launch_fp8_wgrad(int32_t G, const int32_t* m_offsets, int64_t total_m, int64_t P,
+                            int64_t N, int64_t K, Fp8Operand a, Fp8Operand b, Fp8Out y,
+                            hipStream_t stream) {
+  return by_width(y, [&](auto wide) {
+    return wgrad<decltype(wide)::value>(G, m_offsets, total_m, P, N, K, a, b, y, stream);
+  });
+}
+
+}  // namespace nvfp4

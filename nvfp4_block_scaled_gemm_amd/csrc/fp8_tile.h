@@ -1,0 +1,296 @@
+// One output tile of an FP8 block-128 product on the gfx950 matrix cores:
+//
+//   y[m, n] = sum_kb sa[kb, m] * sb[kb, n / b_rows] * sum_{k in block kb} qa[m, k] qb[n, k]
+//
+// E4M3 products are exact in fp32 and v_mfma_f32_16x16x128_f8f6f4 takes one
+// whole block of 128 per instruction, so each instruction starts from zero
+// and its result is one block's sum; the two fp32 scales multiply that sum
+// on the vector unit as it is added to the fp32 accumulator (4 v_fma per
+// matrix instruction of 32 cycles: 16 cycles on the vector unit, which runs
+// beside the matrix core).  The 8-bit matrix rate is only reached through
+// this instruction: the older 16x16x32 form runs at the 16-bit rate.
+//
+//  * A stage is one block of K: BM + BN rows of 128 bytes and one fp32 scale
+//    per row, moved HBM -> LDS by direct loads into a ring.  Rows are
+//    XOR-swizzled in 16-byte chunks so fragment reads spread over the banks;
+//    the swizzle is applied to each lane's source address.
+//  * The weights are the instruction's row operand and the activations its
+//    column operand, so a lane's four results are four neighbouring output
+//    columns of one token and the token's scale is one value per lane.  Rows
+//    of W are dealt to the fragments so that two fragments give a lane eight
+//    neighbouring columns: one 16-byte store of bf16.
+//  * The accumulators must live in the 256 vector registers the vector unit
+//    reaches (it adds into them), which bounds a wave to 128 x 64 outputs.
+//  * WIDE (fp32 outputs) runs the block on the fp16 instructions instead,
+//    which keep fp32 sums, at half the rate (fp8_device.h has the figures).
+//  * Rows past the operand read as zeros by the descriptors' range; a last
+//    block shorter than 128 reads zeros past K in both operands (K % 16 == 0,
+//    so a 16-byte chunk is wholly inside or outside).
+#pragma once
+
+#include "fp8_device.h"
+
+namespace nvfp4 {
+namespace fp8 {
+
+// One operand of a tile: rows of `q` (row stride `ld` bytes, given to run())
+// and the scales of block kb at s + kb * s_ld.
+struct TileOperand {
+  const uint8_t* q;      // tile's first row (gathered: the whole operand)
+  const float* s;        // scale of the tile's first row, block 0 (gathered: of row 0)
+  int64_t s_ld;          // scales per block of K
+  uint32_t q_bytes;      // readable bytes from q
+  uint32_t s_bytes;      // readable bytes from s + kb * s_ld
+  const int32_t* index;  // gathered rows (nullptr: rows in order)
+  int32_t index_n;       // rows of the tile
+  int32_t index_max;     // rows of the operand
+};
+
+struct TileOut {
+  void* y;        // element (0, 0) of the tile
+  int64_t ld;     // elements
+  int32_t m, n;   // rows and columns of the tile that exist
+  int dtype;      // 0 fp32, 1 bf16
+  bool add;       // fp32: y += product
+  bool vec;       // rows are 16-byte aligned
+};
+
+template <int BM, int BN, int WM, int WN, int STAGES, bool BROWS, bool WIDE>
+struct Tile {
+  static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+  static constexpr int TM = BM / WM, TN = BN / WN;
+  static constexpr int FM = TM / 16, FN = TN / 16;
+  static constexpr int kALoads = BM / 8 / kWaves, kBLoads = BN / 8 / kWaves;
+  static constexpr int kScales = (BM + BN) / 64;  // scale-load instructions of a stage
+  static constexpr int kSLoads = (kScales + kWaves - 1) / kWaves;
+  static constexpr int kLoads = kALoads + kBLoads + kSLoads;  // per wave and stage
+  static constexpr int kAOff = 0, kBOff = BM * kBlock, kSOff = (BM + BN) * kBlock;
+  static constexpr int kStage = kSOff + (BM + BN) * 4;
+  static constexpr int kSmem = STAGES * kStage;
+  static_assert(BM % (8 * kWaves) == 0 && BN % (8 * kWaves) == 0, "whole loads per wave");
+  static_assert(BM % 64 == 0 && BN % 64 == 0 && TN % 32 == 0 && TM % 16 == 0, "fragment shapes");
+  static_assert(BROWS || 128 % TN == 0, "one weight scale per wave and block");
+  static_assert((STAGES - 2) * kLoads < 64, "vmcnt range");
+
+  // 16 lanes of an activation fragment read rows r .. r + 15: two rows share
+  // a 256-byte bank line, so the chunk moves with row / 2.
+  static __device__ __forceinline__ int swz_a(int r) { return (r >> 1) & 7; }
+  // 16 lanes of a weight fragment read rows 8 * (l / 4) + l % 4 (+ 4): the
+  // chunk moves with row bits 1, 3 and 4.
+  static __device__ __forceinline__ int swz_b(int r) { return ((r >> 1) & 1) | ((r >> 2) & 6); }
+
+  // K: elements of the sum; ld: bytes between rows of both operands.
+  template <bool GATHER>
+  static __device__ __forceinline__ void run(const TileOperand& A, const TileOperand& B, uint32_t K,
+                                             uint32_t ld, const TileOut& out, uint8_t* smem) {
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    const int li = lane & 15, lg = lane >> 4;
+    const int nk = (int)((K + kBlock - 1) / kBlock);
+
+    uint32_t a_off[kALoads], b_off[kBLoads], s_off[kSLoads];
+    uint32_t a_chunk[kALoads], b_chunk[kBLoads];
+#pragma unroll
+    for (int i = 0; i < kALoads; ++i) {
+      const int r = (wave * kALoads + i) * 8 + (lane >> 3);
+      a_chunk[i] = (uint32_t)(((lane & 7) ^ swz_a(r)) << 4);
+      uint32_t row = (uint32_t)r;
+      bool ok = true;
+      if constexpr (GATHER) {
+        const int32_t v = r < A.index_n ? A.index[r] : -1;
+        ok = v >= 0 && v < A.index_max;
+        row = (uint32_t)v;
+      }
+      a_off[i] = ok ? row * ld + a_chunk[i] : kNoRow;
+    }
+#pragma unroll
+    for (int i = 0; i < kBLoads; ++i) {
+      const int r = (wave * kBLoads + i) * 8 + (lane >> 3);
+      b_chunk[i] = (uint32_t)(((lane & 7) ^ swz_b(r)) << 4);
+      b_off[i] = (uint32_t)r * ld + b_chunk[i];
+    }
+    // scale loads: instruction j < BM / 64 takes the activations' rows, the
+    // others the weights'; waves past the last repeat one (same bytes, same
+    // place), so every wave issues the same number of loads
+    bool s_is_a[kSLoads];
+    int s_slot[kSLoads];
+#pragma unroll
+    for (int i = 0; i < kSLoads; ++i) {
+      const int j = (wave * kSLoads + i) % kScales;
+      s_slot[i] = j;
+      s_is_a[i] = j < BM / 64;
+      const int r = (s_is_a[i] ? j : j - BM / 64) * 64 + lane;
+      if (s_is_a[i]) {
+        uint32_t row = (uint32_t)r;
+        bool ok = true;
+        if constexpr (GATHER) {
+          const int32_t v = r < A.index_n ? A.index[r] : -1;
+          ok = v >= 0 && v < A.index_max;
+          row = (uint32_t)v;
+        }
+        s_off[i] = ok ? row * 4 : kNoRow;
+      } else {
+        s_off[i] = (uint32_t)(BROWS ? r : r / kBlock) * 4;
+      }
+    }
+
+    // the loads of stage s into ring slot `slot`; past the last stage every
+    // lane is out of range (zeros into a slot that is not read again)
+    auto issue = [&](int s, int slot) {
+      uint8_t* base = smem + slot * kStage;
+      const bool live = s < nk;
+      const uint32_t soff = (uint32_t)s * kBlock;
+      const auto ra = make_rsrc(A.q, live ? A.q_bytes : 0u);
+      const auto rb = make_rsrc(B.q, live ? B.q_bytes : 0u);
+      const uint32_t left = K - soff;  // bytes of K from this stage on
+      if (left >= kBlock || !live) {
+#pragma unroll
+        for (int i = 0; i < kALoads; ++i)
+          load_lds16(ra, base + kAOff + (wave * kALoads + i) * 1024, a_off[i], soff);
+#pragma unroll
+        for (int i = 0; i < kBLoads; ++i)
+          load_lds16(rb, base + kBOff + (wave * kBLoads + i) * 1024, b_off[i], soff);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kALoads; ++i)
+          load_lds16(ra, base + kAOff + (wave * kALoads + i) * 1024,
+                     a_chunk[i] < left ? a_off[i] : kNoRow, soff);
+#pragma unroll
+        for (int i = 0; i < kBLoads; ++i)
+          load_lds16(rb, base + kBOff + (wave * kBLoads + i) * 1024,
+                     b_chunk[i] < left ? b_off[i] : kNoRow, soff);
+      }
+#pragma unroll
+      for (int i = 0; i < kSLoads; ++i) {
+        const TileOperand& o = s_is_a[i] ? A : B;
+        load_lds4(make_rsrc(o.s + (live ? s * o.s_ld : 0), live ? o.s_bytes : 0u),
+                  base + kSOff + s_slot[i] * 256, s_off[i], 0);
+      }
+    };
+
+    f32x4 acc[FN][FM];
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+      for (int j = 0; j < FM; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    // LDS addresses of the fragments: a lane takes chunks lg and lg + 4 of
+    // its row in both operands
+    const int b_row0 = wn * TN + 8 * (li >> 2) + (li & 3);
+    auto read_b = [&](const uint8_t* st, int i) {
+      const int r = b_row0 + 32 * (i >> 1) + 4 * (i & 1);
+      const uint8_t* p = st + kBOff + r * kBlock;
+      const int sw = swz_b(r);
+      return join(*reinterpret_cast<const u32x4*>(p + ((lg ^ sw) << 4)),
+                  *reinterpret_cast<const u32x4*>(p + (((lg + 4) ^ sw) << 4)));
+    };
+    auto read_a = [&](const uint8_t* st, int j) {
+      const int r = wm * TM + 16 * j + li;
+      const uint8_t* p = st + kAOff + r * kBlock;
+      const int sw = swz_a(r);
+      return join(*reinterpret_cast<const u32x4*>(p + ((lg ^ sw) << 4)),
+                  *reinterpret_cast<const u32x4*>(p + (((lg + 4) ^ sw) << 4)));
+    };
+
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) issue(s, s);
+    int slot = 0;
+    for (int s = 0; s < nk; ++s) {
+      wait_vmcnt<(STAGES - 2) * kLoads>();
+      workgroup_barrier();
+      // every wave is past stage s - 1: its slot takes stage s + STAGES - 1
+      issue(s + STAGES - 1, slot == 0 ? STAGES - 1 : slot - 1);
+      const uint8_t* st = smem + slot * kStage;
+      const float* sc = reinterpret_cast<const float*>(st + kSOff);
+      decltype(fragment<WIDE>(i32x8{})) bf[FN];
+#pragma unroll
+      for (int i = 0; i < FN; ++i) bf[i] = fragment<WIDE>(read_b(st, i));
+      float fa[FM];
+#pragma unroll
+      for (int j = 0; j < FM; ++j) fa[j] = sc[wm * TM + 16 * j + li];
+      f32x4 fb[BROWS ? FN : 1];
+      if constexpr (BROWS) {
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+          fb[i] = *reinterpret_cast<const f32x4*>(sc + BM + wn * TN + 32 * (i >> 1) + 8 * lg + 4 * (i & 1));
+      } else {
+        const float f = sc[BM + wn * TN];
+#pragma unroll
+        for (int j = 0; j < FM; ++j) fa[j] *= f;
+      }
+#pragma unroll
+      for (int j = 0; j < FM; ++j) {
+        const auto af = fragment<WIDE>(read_a(st, j));
+#pragma unroll
+        for (int i = 0; i < FN; ++i) {
+          const f32x4 c = mfma_block(bf[i], af);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float f = BROWS ? fb[BROWS ? i : 0][e] * fa[j] : fa[j];
+            acc[i][j][e] = __builtin_fmaf(c[e], f, acc[i][j][e]);
+          }
+        }
+      }
+      slot = slot + 1 == STAGES ? 0 : slot + 1;
+    }
+    // the ring's last loads land before the slots can be written again
+    wait_vmcnt<0>();
+
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      const int m = wm * TM + 16 * j + li;
+      if (m >= out.m) continue;
+#pragma unroll
+      for (int p = 0; p < FN / 2; ++p) {
+        const int n = wn * TN + 32 * p + 8 * lg;
+        if (n >= out.n) continue;
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] = acc[2 * p][j][e];
+          v[4 + e] = acc[2 * p + 1][j][e];
+        }
+        store8(out, m, n, v);
+      }
+    }
+  }
+
+  // Eight neighbouring outputs of one row (those below out.n).
+  static __device__ __forceinline__ void store8(const TileOut& out, int m, int n, const float* v) {
+    const int64_t at = (int64_t)m * out.ld + n;
+    if (out.vec && n + 8 <= out.n) {
+      if (out.dtype == 1) {
+        u32x4 w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          w[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(
+                                                  f32x2{v[2 * e], v[2 * e + 1]}, bf16x2));
+        *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(out.y) + at) = w;
+      } else {
+        f32x4* p = reinterpret_cast<f32x4*>(reinterpret_cast<float*>(out.y) + at);
+        f32x4 lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
+        if (out.add) {
+          lo += p[0];
+          hi += p[1];
+        }
+        p[0] = lo;
+        p[1] = hi;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (n + e < out.n) {
+          if (out.dtype == 1) {
+            reinterpret_cast<__bf16*>(out.y)[at + e] = (__bf16)v[e];
+          } else {
+            float* p = reinterpret_cast<float*>(out.y) + at + e;
+            *p = out.add ? *p + v[e] : v[e];
+          }
+        }
+    }
+  }
+};
+
+}  // namespace fp8
+}  // namespace nvfp4

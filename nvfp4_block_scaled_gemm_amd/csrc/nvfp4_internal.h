@@ -111,4 +111,69 @@ hipError_t launch_gemm_grouped(int32_t G, const int32_t* m_offsets, const int32_
                                PackedOperand a, PackedOperand b, void* y, int y_dtype,
                                int64_t ld_y, hipStream_t stream);
 
+// FP8 block-128 operand [rows, K] and output (fp8_gemm.hip).
+struct Fp8Operand {
+  const uint8_t* q;  // E4M3 bytes [rows, K]
+  const float* s;    // [ceil(K / 128), ceil(rows / block_rows)]
+};
+struct Fp8Out {
+  void* y;
+  int64_t ld;  // elements
+  int dtype;   // 0 fp32, 1 bf16
+  bool add;    // fp32 only: y += product
+  bool vec;    // rows start on 16-byte borders
+};
+
+// Columns of an expert-wise transposed operand: total_m tokens of G experts,
+// each expert's starting on a border of 128 (an upper bound known on the
+// host; the experts' counts are not).
+inline int64_t fp8_padded_tokens(int64_t total_m, int64_t G) {
+  const int64_t g = G < total_m ? G : total_m;
+  return (total_m + 127 * g) / 128 * 128;
+}
+
+// fp8_quantize.hip: rows layout q/s and transposed layout qt/st (either may
+// be null).
+hipError_t launch_fp8_quantize(const void* x, int dtype, int64_t batch, int64_t rows, int64_t cols,
+                               int64_t ld_x, int block_rows, uint8_t* q, float* s, uint8_t* qt,
+                               float* st, hipStream_t stream);
+hipError_t launch_fp8_grouped_quantize(const void* x, int dtype, int32_t G,
+                                       const int32_t* m_offsets, const int32_t* row_index,
+                                       int64_t total_m, int64_t x_rows, int64_t cols, int64_t ld_x,
+                                       uint8_t* q, float* s, uint8_t* qt, float* st,
+                                       hipStream_t stream);
+// fp8_gemm.hip: K % 16 == 0, K <= 2^22, 16-byte aligned q.
+hipError_t launch_fp8_gemm(int64_t M, int64_t N, int64_t K, Fp8Operand a, Fp8Operand b,
+                           int b_block_rows, Fp8Out y, hipStream_t stream);
+// row_index != nullptr: a_rows * K < 2^31
+hipError_t launch_fp8_grouped(int32_t G, const int32_t* m_offsets, const int32_t* row_index,
+                              int64_t total_m, int64_t a_rows, int64_t N, int64_t K, Fp8Operand a,
+                              Fp8Operand b, Fp8Out y, hipStream_t stream);
+// P: columns of the transposed operands (fp8_padded_tokens)
+hipError_t launch_fp8_wgrad(int32_t G, const int32_t* m_offsets, int64_t total_m, int64_t P,
+                            int64_t N, int64_t K, Fp8Operand a, Fp8Operand b, Fp8Out y,
+                            hipStream_t stream);
+
+// moe_route.hip
+struct RouteOut {
+  int32_t* expert_index;  // [T, k]
+  float* weights;         // [T, k]
+  int32_t* counts;        // [E]
+  int32_t* m_offsets;     // [E + 1]
+  int32_t* row_index;     // [T * k]
+  int32_t* pair_row;      // [T, k]
+  int32_t* routed;        // [1]
+  float* loss;            // [1]
+};
+size_t moe_route_workspace_bytes(int64_t T, int64_t E);
+hipError_t launch_moe_route(int64_t T, int64_t E, int topk, const void* logits, int dtype,
+                            int64_t ld, const uint8_t* mask, bool renorm, RouteOut out,
+                            void* workspace, hipStream_t stream);
+hipError_t launch_moe_route_backward(int64_t T, int64_t E, int topk, const void* logits, int dtype,
+                                     int64_t ld, const uint8_t* mask, bool renorm,
+                                     const int32_t* expert_index, const int32_t* counts,
+                                     const int32_t* routed, const float* d_weights,
+                                     const float* d_loss, void* d_logits, int64_t ld_d,
+                                     hipStream_t stream);
+
 }  // namespace nvfp4

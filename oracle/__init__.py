@@ -12,3 +12,8 @@ from .nvfp4_ref import (  # noqa: F401
 from .mxfp4_ref import (  # noqa: F401
     MX_BLOCK, e8m0_decode, mxfp4_dequantize_ref, mxfp4_gemm_ref, mxfp4_quantize_ref,
 )
+from .fp8_ref import (  # noqa: F401
+    E4M3_TABLE, FP8_BLOCK, e4m3_encode, fp8_dequantize_ref, fp8_gemm_ref, fp8_grouped_columns_ref,
+    fp8_grouped_quantize_t_ref, fp8_quantize_ref, fp8_quantize_t_ref, fp8_tolerance,
+    moe_route_backward_ref, moe_route_ref,
+)

@@ -1,0 +1,399 @@
+"""FP8 block-128 operators on the GPU against the fp64 oracle: the quantisers
+byte for byte, the products within the error of fp32 accumulation
+(oracle.fp8_tolerance derives it)."""
+import numpy as np
+import pytest
+import torch
+
+import nvfp4_block_scaled_gemm_amd as nv
+import workloads as wl
+from oracle import (fp8_dequantize_ref, fp8_gemm_ref, fp8_grouped_quantize_t_ref, fp8_quantize_ref, fp8_quantize_t_ref,
+                    fp8_tolerance)
+from tests.gpu_util import need_gpu, note, np_
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    need_gpu()
+
+
+def bytes_of(q):
+    return np_(q.view(torch.uint8))
+
+
+def same(op, ref):
+    q, s = bytes_of(op[0]), np_(op[1])
+    rq, rs = ref
+    assert q.shape == rq.shape and s.shape == rs.shape
+    assert np.array_equal(s, rs, equal_nan=True), np.argwhere(s != rs)[:4]
+    assert np.array_equal(q, rq), np.argwhere(q != rq)[:4]
+
+
+def values(rows, cols, seed, dtype="bf16", spread=8.0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(rows, cols, generator=g)
+    x = x * torch.exp2(torch.randint(-int(spread), int(spread) + 1, (rows, 1), generator=g).float())
+    return x.to(torch.bfloat16) if dtype == "bf16" else x
+
+
+# ---- quantisers -------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("rows,cols", [(1, 16), (1, 128), (7, 144), (64, 256), (129, 400), (200, 2064)])
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_quantize_both_layouts(dtype, rows, cols, block_rows):
+    x = values(rows, cols, rows + cols, dtype)
+    note(f"fp8 quantize {dtype} {rows}x{cols} block_rows {block_rows}")
+    r, t = nv.nvfp4_fp8_quantize(x.to(DEV), block_rows=block_rows, layout="both")
+    only_r = nv.nvfp4_fp8_quantize(x.to(DEV), block_rows=block_rows)
+    only_t = nv.nvfp4_fp8_quantize(x.to(DEV), block_rows=block_rows, layout="cols")
+    ref, ref_t = fp8_quantize_ref(x.float().numpy(), block_rows), fp8_quantize_t_ref(x.float().numpy(), block_rows)
+    same(r, ref)
+    same(only_r, ref)
+    same(t, ref_t)
+    same(only_t, ref_t)
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_quantize_special_blocks(block_rows):
+    x = torch.zeros(260, 384)
+    x[1, 3], x[2, 200], x[130, 130] = float("nan"), float("inf"), -float("inf")
+    x[3], x[4, :128], x[5, 0] = 1e-40, 3e38, -0.0
+    x[140:, 256:] = torch.randn(120, 128, generator=torch.Generator().manual_seed(1)) * 1e-30
+    note(f"fp8 quantize special blocks {block_rows}")
+    r, t = nv.nvfp4_fp8_quantize(x.to(DEV), block_rows=block_rows, layout="both")
+    same(r, fp8_quantize_ref(x.numpy(), block_rows))
+    same(t, fp8_quantize_t_ref(x.numpy(), block_rows))
+
+
+def test_quantize_batches_strides_and_out():
+    w = torch.stack([values(200, 272, 5 + i, "fp32") for i in range(3)])
+    note("fp8 quantize batch")
+    r, t = nv.nvfp4_fp8_quantize(w.to(DEV), block_rows=128, layout="both")
+    r1 = nv.nvfp4_fp8_quantize(w.to(DEV), block_rows=1)
+    for i in range(3):
+        same((r[0][i], r[1][i]), fp8_quantize_ref(w[i].numpy(), 128))
+        same((t[0][i], t[1][i]), fp8_quantize_t_ref(w[i].numpy(), 128))
+        same((r1[0][i], r1[1][i]), fp8_quantize_ref(w[i].numpy(), 1))
+    wide = values(50, 512, 9)
+    out = nv.nvfp4_fp8_quantize(wide.to(DEV)[:, 64:64 + 160].contiguous())
+    note("fp8 quantize strided rows into given buffers")
+    got = nv.nvfp4_fp8_quantize(wide.to(DEV)[:, 64:64 + 160], out=out)
+    assert got[0].data_ptr() == out[0].data_ptr()
+    same(got, fp8_quantize_ref(wide[:, 64:224].float().numpy()))
+    assert nv.nvfp4_fp8_quantize(torch.empty(0, 64, device=DEV))[0].shape == (0, 64)
+
+
+@pytest.mark.parametrize("counts", [[5], [0, 128, 0, 1, 129], [300, 0, 0], [1] * 70, [0, 0]])
+@pytest.mark.parametrize("gather", [False, True])
+def test_grouped_quantize(counts, gather):
+    off = wl.ragged_offsets(counts)
+    total = int(off[-1])
+    src = values(max(total, 1), 144, total + gather)[:max(total, 1) if gather else total]
+    idx = torch.randint(-1, src.shape[0] + 1, (total,), generator=torch.Generator().manual_seed(2)).int()
+    x = src.float()
+    if gather:
+        x = torch.where(((idx >= 0) & (idx < src.shape[0]))[:, None], x[idx.long().clamp(0, src.shape[0] - 1)], 0.0)
+    note(f"fp8 grouped quantize {counts[:6]} gather {gather}")
+    r, t = nv.nvfp4_fp8_grouped_quantize(src.to(DEV), off.to(DEV), layout="both",
+                                         row_index=idx.to(DEV) if gather else None)
+    if total == 0:
+        assert r[0].shape == (0, 144) and t[0].shape == (144, 0)
+        return
+    same(r, fp8_quantize_ref(x.numpy()))
+    same(t, fp8_grouped_quantize_t_ref(x.numpy(), off.tolist()))
+
+
+def test_grouped_quantize_leaves_rows_of_no_group():
+    x = values(40, 128, 3)
+    off = torch.tensor([0, 10, 25], dtype=torch.int32)
+    q = torch.full((40, 128), 0x11, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+    s = torch.full((1, 40), -3.0, device=DEV)
+    note("fp8 grouped quantize, rows behind the last group")
+    nv.nvfp4_fp8_grouped_quantize(x.to(DEV), off.to(DEV), layout="rows", out=(q, s))
+    assert (bytes_of(q)[25:] == 0x11).all() and (np_(s)[:, 25:] == -3.0).all()
+    rq, rs = fp8_quantize_ref(x[:25].float().numpy())
+    assert np.array_equal(bytes_of(q)[:25], rq) and np.array_equal(np_(s)[:, :25], rs)
+
+
+# ---- products ---------------------------------------------------------------
+
+def rand_operand(rng, rows, K, block_rows=1, lead=()):
+    """Random finite E4M3 bytes and scales over three decades."""
+    q = rng.integers(0, 256, (*lead, rows, K)).astype(np.uint8)
+    q[(q & 0x7F) == 0x7F] = 0x3C
+    s = np.exp2(rng.uniform(-8, 2, (*lead, -(-K // 128), -(-rows // block_rows)))).astype(np.float32)
+    return q, s
+
+
+def to_gpu(op):
+    return (torch.from_numpy(op[0]).to(DEV).view(torch.float8_e4m3fn), torch.from_numpy(op[1]).to(DEV))
+
+
+def close(y, a, b, block_rows, out, rows=None, add=None):
+    """y against the oracle; rows: the rows of y and a that are checked."""
+    aq, sa = (a[0], a[1]) if rows is None else (a[0][rows], a[1][:, rows])
+    ref, base = fp8_gemm_ref(aq, sa, b[0], b[1], block_rows)
+    tol = fp8_tolerance(ref, base, fp8_dequantize_ref(aq, sa), fp8_dequantize_ref(b[0], b[1], block_rows), out)
+    if add is not None:          # one more fp32 addition
+        ref = ref + add
+        tol = tol + 2.0 ** -24 * (np.abs(ref) + tol)
+    got = np_(y).astype(np.float64)
+    got = got if rows is None else got[rows]
+    bad = np.argwhere(~(np.abs(got - ref) <= tol))
+    assert bad.size == 0, (bad[:4].tolist(), got[tuple(bad[0])], ref[tuple(bad[0])], tol[tuple(bad[0])])
+
+
+SHAPES = [(1, 1, 16), (1, 300, 128), (2, 17, 144), (3, 256, 1024), (5, 8, 2064), (16, 128, 256), (17, 200, 512),
+          (31, 130, 400), (33, 1000, 640), (48, 64, 8192), (64, 96, 272), (65, 129, 1040), (100, 513, 384),
+          (128, 128, 128), (130, 4100, 256), (200, 333, 1552), (257, 640, 112)]
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_gemm(M, N, K, block_rows, out):
+    rng = np.random.default_rng(M * 7 + N * 3 + K)
+    a, b = rand_operand(rng, M, K), rand_operand(rng, N, K, block_rows)
+    note(f"fp8 gemm {M}x{N}x{K} block_rows {block_rows} {out}")
+    y = nv.nvfp4_fp8_gemm(to_gpu(a), to_gpu(b), out)
+    close(y, a, b, block_rows if N > 1 else 1, out)
+
+
+@pytest.mark.parametrize("M,N,K", [(1024, 1100, 384), (4096, 1024, 256), (2500, 4200, 144), (4096, 4096, 128),
+                                   (8192, 8200, 272)])
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_gemm_many_tiles(M, N, K, block_rows):
+    """Enough tiles for the large tile shapes, ragged edges; sampled rows."""
+    rng = np.random.default_rng(M + N + K)
+    a, b = rand_operand(rng, M, K), rand_operand(rng, N, K, block_rows)
+    note(f"fp8 gemm {M}x{N}x{K} block_rows {block_rows} (many tiles)")
+    y = nv.nvfp4_fp8_gemm(to_gpu(a), to_gpu(b), "f32")
+    rows = np.unique(np.concatenate([[0, 127, 128, 255, 256, M - 1], rng.choice(M, 40, replace=False)]))
+    close(y, a, b, block_rows, "f32", rows=rows)
+
+
+@pytest.mark.parametrize("M,N,K,block_rows", [(1, 512, 512, 128), (40, 300, 272, 1), (300, 257, 384, 1),
+                                              (300, 257, 384, 128)])
+def test_gemm_accumulates(M, N, K, block_rows):
+    rng = np.random.default_rng(M + N)
+    a, b = rand_operand(rng, M, K), rand_operand(rng, N, K, block_rows)
+    y0 = rng.standard_normal((M, N)).astype(np.float32) * 1e3
+    y = torch.from_numpy(y0).to(DEV)
+    note(f"fp8 gemm accumulate {M}x{N}x{K}")
+    assert nv.nvfp4_fp8_gemm(to_gpu(a), to_gpu(b), "f32", y=y, accumulate=True) is y
+    close(y, a, b, block_rows, "f32", add=y0.astype(np.float64))
+
+
+@pytest.mark.parametrize("M", [1, 20, 200])
+@pytest.mark.parametrize("out,ld,shift", [("bf16", 136, 0), ("bf16", 133, 1), ("f32", 132, 0), ("f32", 131, 3)])
+def test_gemm_writes_only_its_view(M, out, ld, shift):
+    """Row strides and bases that allow 16-byte stores and ones that do not;
+    the bytes around y stay."""
+    rng = np.random.default_rng(ld)
+    N, K = 130, 256
+    a, b = rand_operand(rng, M, K), rand_operand(rng, N, K, 128)
+    dt = torch.bfloat16 if out == "bf16" else torch.float32
+    buf = torch.full((M * ld + 64,), 7.0, dtype=dt, device=DEV)
+    y = buf[shift:shift + M * ld].view(M, ld)[:, :N]
+    note(f"fp8 gemm strided y M {M} {out} ld {ld} shift {shift}")
+    nv.nvfp4_fp8_gemm(to_gpu(a), to_gpu(b), out, y=y)
+    close(y, a, b, 128, out)
+    rest = buf.clone()
+    rest[shift:shift + M * ld].view(M, ld)[:, :N] = 7.0
+    assert bool((rest == 7.0).all())
+
+
+@pytest.mark.parametrize("M", [3, 40, 300])
+def test_gemm_exact_codes_and_nan_scales(M):
+    """Every finite code against a unit row: exact; a NaN scale marks its row
+    (or column block) and no other."""
+    K, N = 256, 256
+    rng = np.random.default_rng(M)
+    bq = np.tile(np.arange(256, dtype=np.uint8), (N, 1))
+    bq[:, [0x7F, 0xFF]] = 0
+    b = (bq, np.ones((2, 2), np.float32))
+    aq = np.zeros((M, K), np.uint8)
+    hot = rng.permutation(K)[:M] if M <= K else rng.integers(0, K, M)
+    aq[np.arange(M), hot] = 0x38                     # 1.0
+    a = (aq, np.ones((2, M), np.float32))
+    note(f"fp8 gemm one-hot rows M {M}")
+    y = np_(nv.nvfp4_fp8_gemm(to_gpu(a), to_gpu(b), "f32"))
+    vals = torch.from_numpy(bq).view(torch.float8_e4m3fn).float().numpy()
+    assert np.array_equal(y, vals[:, hot].T)
+    a[1][1, 1] = np.nan
+    b[1][0, 1] = np.nan
+    y = np_(nv.nvfp4_fp8_gemm(to_gpu(a), to_gpu(b), "f32"))
+    assert np.isnan(y[1]).all() and np.isnan(y[:, 128:]).all()
+    assert np.isfinite(np.delete(y, 1, 0)[:, :128]).all()
+
+
+def test_gemm_empty():
+    f8 = torch.float8_e4m3fn
+    a = (torch.empty(4, 0, dtype=f8, device=DEV), torch.empty(0, 4, device=DEV))
+    b = (torch.empty(40, 0, dtype=f8, device=DEV), torch.empty(0, 1, device=DEV))
+    note("fp8 gemm K = 0")
+    y = torch.full((4, 40), 3.0, device=DEV)
+    assert bool((nv.nvfp4_fp8_gemm(a, b, "f32", y=y, accumulate=True) == 3.0).all())
+    assert bool((nv.nvfp4_fp8_gemm(a, b, "f32", y=y) == 0).all())
+    z = (torch.empty(0, 128, dtype=f8, device=DEV), torch.empty(1, 0, device=DEV))
+    w = (torch.empty(8, 128, dtype=f8, device=DEV), torch.empty(1, 1, device=DEV))
+    assert nv.nvfp4_fp8_gemm(z, w).shape == (0, 8)
+
+
+GROUPS = [[5], [0, 3, 0, 40, 1], [16] * 9, [130, 0, 257, 64, 1], [1, 2] * 40, [0, 0, 700], [33, 64, 65, 0]]
+
+
+@pytest.mark.parametrize("counts", GROUPS, ids=lambda c: f"G{len(c)}t{sum(c)}")
+@pytest.mark.parametrize("N,K", [(72, 144), (300, 512), (8, 16)])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_grouped(counts, N, K, gather, out):
+    rng = np.random.default_rng(sum(counts) + N)
+    off = wl.ragged_offsets(counts)
+    total, G = int(off[-1]), len(counts)
+    a_rows = 37 if gather else total
+    a, b = rand_operand(rng, a_rows, K), rand_operand(rng, N, K, 128, (G,))
+    idx = rng.integers(-1, a_rows + 1, total).astype(np.int32)       # -1 and a_rows: a row of zeros
+    note(f"fp8 grouped {len(counts)} groups {total} rows N {N} K {K} gather {gather} {out}")
+    y = np_(nv.nvfp4_fp8_grouped_gemm(off.to(DEV), total, to_gpu(a), to_gpu(b), out,
+                                      row_index=torch.from_numpy(idx).to(DEV) if gather else None))
+    for e in range(G):
+        lo, hi = int(off[e]), int(off[e + 1])
+        if gather:
+            ok = (idx[lo:hi] >= 0) & (idx[lo:hi] < a_rows)
+            q = np.where(ok[:, None], a[0][idx[lo:hi].clip(0, a_rows - 1)], 0)
+            s = np.where(ok[None, :], a[1][:, idx[lo:hi].clip(0, a_rows - 1)], 0).astype(np.float32)
+        else:
+            q, s = a[0][lo:hi], a[1][:, lo:hi]
+        close(torch.from_numpy(y[lo:hi]), (q, s), (b[0][e], b[1][e]), 128, out)
+
+
+def test_grouped_leaves_rows_of_no_group():
+    rng = np.random.default_rng(4)
+    a, b = rand_operand(rng, 50, 128), rand_operand(rng, 40, 128, 128, (2,))
+    off = torch.tensor([0, 7, 30], dtype=torch.int32)
+    y = torch.full((50, 40), 5.0, device=DEV)
+    note("fp8 grouped, rows behind the last group")
+    nv.nvfp4_fp8_grouped_gemm(off.to(DEV), 50, to_gpu(a), to_gpu(b), "f32", y=y)
+    assert bool((y[30:] == 5.0).all())
+    for e, (lo, hi) in enumerate(((0, 7), (7, 30))):
+        close(y[lo:hi], (a[0][lo:hi], a[1][:, lo:hi]), (b[0][e], b[1][e]), 128, "f32")
+
+
+def test_grouped_stays_inside_on_bad_offsets():
+    """Offsets that run backwards or past the rows: nothing outside y is
+    touched and the call ends."""
+    rng = np.random.default_rng(5)
+    a, b = rand_operand(rng, 40, 128), rand_operand(rng, 24, 128, 128, (4,))
+    off = torch.tensor([0, 30, 10, 9000, -5], dtype=torch.int32)
+    buf = torch.full((60, 24), 2.0, device=DEV)
+    note("fp8 grouped, inconsistent offsets")
+    nv.nvfp4_fp8_grouped_gemm(off.to(DEV), 40, to_gpu(a), to_gpu(b), "f32", y=buf[10:50])
+    torch.cuda.synchronize()
+    assert bool((buf[:10] == 2.0).all()) and bool((buf[50:] == 2.0).all())
+
+
+def test_grouped_many_groups_and_past_4_gib():
+    """More groups than a wave has lanes, and expert weights past 2^32 bytes."""
+    G, N, K = 150, 4096, 7168
+    g = torch.Generator(device=DEV).manual_seed(6)
+    q = torch.randint(0, 120, (G, N, K), dtype=torch.uint8, device=DEV, generator=g)
+    s = torch.rand(G, K // 128, N // 128, device=DEV, generator=g)
+    counts = [0] * G
+    counts[0], counts[70], counts[149] = 3, 20, 40
+    off = wl.ragged_offsets(counts)
+    a = rand_operand(np.random.default_rng(6), 63, K)
+    note("fp8 grouped, weights past 4 GiB")
+    y = nv.nvfp4_fp8_grouped_gemm(off.to(DEV), 63, to_gpu(a), (q.view(torch.float8_e4m3fn), s), "f32")
+    for e, lo, hi in ((0, 0, 3), (70, 3, 23), (149, 23, 63)):
+        close(y[lo:hi], (a[0][lo:hi], a[1][:, lo:hi]), (np_(q[e]), np_(s[e])), 128, "f32")
+
+
+@pytest.mark.parametrize("counts", [[5], [0, 130, 0, 1, 256], [128, 128], [0, 0, 0], [300, 7] * 5],
+                         ids=lambda c: f"G{len(c)}t{sum(c)}")
+@pytest.mark.parametrize("N,K", [(48, 80), (144, 272), (16, 128)])
+@pytest.mark.parametrize("out,add", [("f32", False), ("bf16", False), ("f32", True)])
+def test_wgrad(counts, N, K, out, add):
+    off = wl.ragged_offsets(counts)
+    total, G = int(off[-1]), len(counts)
+    dy, x = values(total, N, 1, "fp32"), values(total, K, 2, "bf16")
+    note(f"fp8 wgrad {counts[:6]} N {N} K {K} {out} add {add}")
+    a = nv.nvfp4_fp8_grouped_quantize(dy.to(DEV), off.to(DEV))
+    b = nv.nvfp4_fp8_grouped_quantize(x.to(DEV), off.to(DEV))
+    dw0 = torch.randn(G, N, K, generator=torch.Generator().manual_seed(3)) * 100 if add else None
+    dw = np_(nv.nvfp4_fp8_grouped_wgrad(off.to(DEV), total, a, b, out,
+                                        dw=dw0.to(DEV) if add else None, accumulate=add))
+    aq, sa, bq, sb = bytes_of(a[0]), np_(a[1]), bytes_of(b[0]), np_(b[1])
+    at = 0
+    for e, c in enumerate(counts):
+        n = -(-c // 128) * 128
+        part = lambda q, s: (q[:, at:at + n], s[at // 128:(at + n) // 128])  # noqa: E731
+        if c == 0:
+            assert np.array_equal(dw[e], dw0[e].numpy() if add else np.zeros((N, K)))
+        else:
+            close(torch.from_numpy(dw[e]), part(aq, sa), part(bq, sb), 1, out,
+                  add=dw0[e].double().numpy() if add else None)
+        at += n
+
+
+# ---- streams, graphs --------------------------------------------------------
+
+def test_side_stream_and_graph_replays():
+    """Quantise -> product -> accumulate on a side stream, and captured and
+    replayed with new inputs beside the program's own eager work."""
+    M, N, K = 70, 260, 512
+    xs = [values(M, K, 20 + i).to(DEV) for i in range(4)]
+    w = nv.nvfp4_fp8_quantize(values(N, K, 30, spread=1).to(DEV), block_rows=128)
+    eager = [nv.nvfp4_fp8_gemm(nv.nvfp4_fp8_quantize(x), w, "f32") for x in xs]
+    side = torch.cuda.Stream()
+    note("fp8 on a side stream")
+    side.wait_stream(torch.cuda.current_stream())
+    a = nv.nvfp4_fp8_quantize(xs[0], stream=side)
+    y = nv.nvfp4_fp8_gemm(a, w, "f32", stream=side)
+    side.synchronize()
+    assert torch.equal(y, eager[0])
+    xin = xs[0].clone()
+    note("fp8 captured")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q = nv.nvfp4_fp8_quantize(xin)
+        yg = nv.nvfp4_fp8_gemm(q, w, "f32")
+    for i in (1, 2, 3, 0, 2):
+        xin.copy_(xs[i])
+        graph.replay()
+        again = nv.nvfp4_fp8_gemm(nv.nvfp4_fp8_quantize(xs[i]), w, "f32")
+        torch.cuda.synchronize()
+        assert torch.equal(yg, eager[i]) and torch.equal(again, eager[i])
+
+
+def test_results_do_not_change_between_calls():
+    off = wl.ragged_offsets([40, 0, 200, 3])
+    rng = np.random.default_rng(8)
+    a, b = to_gpu(rand_operand(rng, 243, 272)), to_gpu(rand_operand(rng, 144, 272, 128, (4,)))
+    note("fp8 grouped twice")
+    one = nv.nvfp4_fp8_grouped_gemm(off.to(DEV), 243, a, b, "f32")
+    two = nv.nvfp4_fp8_grouped_gemm(off.to(DEV), 243, a, b, "f32")
+    assert torch.equal(one, two)
+
+
+def test_wrappers_refuse_operands_that_do_not_fit():
+    a = nv.nvfp4_fp8_quantize(values(4, 256, 1).to(DEV))
+    w = nv.nvfp4_fp8_quantize(values(300, 256, 2).to(DEV), block_rows=128)
+    other = nv.nvfp4_fp8_quantize(values(4, 128, 1).to(DEV))
+    y = torch.empty(4, 300, dtype=torch.bfloat16, device=DEV)
+    for call in (lambda: nv.nvfp4_fp8_gemm(other, w), lambda: nv.nvfp4_fp8_gemm(w, a),
+                 lambda: nv.nvfp4_fp8_gemm(a, w, "f16"), lambda: nv.nvfp4_fp8_gemm(a, w, "f32", y=y),
+                 lambda: nv.nvfp4_fp8_gemm(a, w, "bf16", y=y, accumulate=True),
+                 lambda: nv.nvfp4_fp8_gemm(a, w, y=y[:, :299]),
+                 lambda: nv.nvfp4_fp8_gemm(a, w, "f32", accumulate=True),
+                 lambda: nv.nvfp4_fp8_quantize(torch.empty(4, 24, device=DEV)),
+                 lambda: nv.nvfp4_fp8_quantize(torch.empty(4, 32, device=DEV), layout="up")):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(nv.Nvfp4Error):
+        nv.nvfp4_fp8_quantize(torch.empty(4, 34, device=DEV)[:, 2:])   # rows 8 bytes off a 16-byte border
