@@ -36,7 +36,7 @@ __device__ __forceinline__ TileOut out_of(const Fp8Out& y, int64_t at, int m, in
 }
 
 template <int BM, int BN, int WM, int WN, int STAGES, bool BROWS, bool WIDE>
-__global__ __launch_bounds__(64 * WM * WN) void fp8_dense_kernel(int64_t M, int64_t N, int64_t K,
+__global__ __launch_bounds__(64 * WM * WN, 2) void fp8_dense_kernel(int64_t M, int64_t N, int64_t K,
                                                                  Fp8Operand a, Fp8Operand b,
                                                                  Fp8Out y) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -58,7 +58,7 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_dense_kernel(int64_t M, int6
 // list is known on the device only: each wave keeps 64 experts' running tile
 // counts in its lanes and finds a tile's expert by one ballot.
 template <int BM, int BN, int WM, int WN, int STAGES, bool GATHER, bool WIDE>
-__global__ __launch_bounds__(64 * WM * WN) void fp8_grouped_kernel(
+__global__ __launch_bounds__(64 * WM * WN, 2) void fp8_grouped_kernel(
     int G, const int32_t* __restrict__ offsets, const int32_t* __restrict__ row_index,
     int64_t total_m, int64_t a_rows, int64_t N, int64_t K, Fp8Operand a, Fp8Operand b, Fp8Out y) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -108,7 +108,7 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_grouped_kernel(
 // dW_e = A_e . B_e^T over the expert's own columns of the transposed
 // operands; each expert's columns start on a block border.
 template <int BM, int BN, int WM, int WN, int STAGES, bool WIDE>
-__global__ __launch_bounds__(64 * WM * WN) void fp8_wgrad_kernel(
+__global__ __launch_bounds__(64 * WM * WN, 2) void fp8_wgrad_kernel(
     int G, const int32_t* __restrict__ offsets, int64_t total_m, int64_t P, int64_t N, int64_t K,
     Fp8Operand a, Fp8Operand b, Fp8Out y) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -145,45 +145,116 @@ hipError_t allow_lds(Kern kern, int bytes, std::atomic<uint64_t>& done) {
   return e;
 }
 
-template <bool BROWS, bool WIDE>
+// A tile shape: BM x BN outputs by WM x WN waves with a ring of S stages.
+template <int BM_, int BN_, int WM_, int WN_, int S_>
+struct Shape {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_;
+};
+using S256x256 = Shape<256, 256, 2, 4, 2>;
+using S128x256 = Shape<128, 256, 2, 4, 3>;
+using S128x128 = Shape<128, 128, 2, 2, 2>;
+using S128x64 = Shape<128, 64, 2, 2, 3>;
+using S64x128 = Shape<64, 128, 2, 2, 3>;
+using S64x64 = Shape<64, 64, 2, 2, 4>;
+
+template <typename S, bool BROWS, bool WIDE>
 hipError_t dense(int64_t M, int64_t N, int64_t K, Fp8Operand a, Fp8Operand b, Fp8Out y,
                  hipStream_t stream) {
-  constexpr int BM = 128, BN = 128, S = 2;
-  using T = Tile<BM, BN, 2, 2, S, BROWS, WIDE>;
-  auto kern = fp8_dense_kernel<BM, BN, 2, 2, S, BROWS, WIDE>;
+  using T = Tile<S::BM, S::BN, S::WM, S::WN, S::S, BROWS, WIDE>;
+  auto kern = fp8_dense_kernel<S::BM, S::BN, S::WM, S::WN, S::S, BROWS, WIDE>;
   static std::atomic<uint64_t> done{0};
   const hipError_t err = allow_lds(kern, T::kSmem, done);
   if (err != hipSuccess) return err;
-  const int64_t tiles = ((M + BM - 1) / BM) * ((N + BN - 1) / BN);
+  const int64_t tiles = ((M + S::BM - 1) / S::BM) * ((N + S::BN - 1) / S::BN);
   if (tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
   kern<<<(unsigned)tiles, T::kThreads, T::kSmem, stream>>>(M, N, K, a, b, y);
   return hipGetLastError();
 }
 
-template <bool GATHER, bool WIDE>
+// Time of a shape in units of 0.01 us per block of K, from the tiles that the
+// busiest of 256 CUs gets: t1 for one tile alone on a CU, t2 for two (shapes
+// of which one fits a CU: twice t1).
+int64_t shape_cost(int64_t M, int64_t N, int64_t bm, int64_t bn, int64_t t1, int64_t t2) {
+  const int64_t tiles = ((M + bm - 1) / bm) * ((N + bn - 1) / bn);
+  const int64_t n = (tiles + 255) / 256;
+  return n / 2 * t2 + n % 2 * t1;
+}
+
+// The shape with the least expected time.  Measured (us per block of 128,
+// one / two tiles on each CU): 8-bit products 256 x 256 1.70 / 3.40, 128 x 256
+// 1.18 / 2.36, 128 x 128 0.90 / 1.22, 128 x 64 0.49 / 0.75, 64 x 64
+// 0.36 / 0.55; wide ones 128 x 128 1.26 / 2.06, 128 x 64 0.79 / 1.27, 64 x 64
+// 0.60 / 0.80 (their larger shapes spill).  So 4096 x 8192 takes 256 x 256
+// (230 us at K = 8192; 128 x 256: 290), 1024 x 8192 takes 128 x 256 (75;
+// 256 x 256: 99), 512 x 4096 takes 128 x 64 (24.4 at K = 6144; 128 x 128:
+// 41.8), 96 x 8192 takes 64 x 64 (23.3; 128 x 64: 30.7).
+template <bool BROWS, bool WIDE>
+hipError_t dense_any(int64_t M, int64_t N, int64_t K, Fp8Operand a, Fp8Operand b, Fp8Out y,
+                     hipStream_t stream) {
+  constexpr int kShapes = WIDE ? 3 : 5;
+  int64_t cost[kShapes];
+  if constexpr (WIDE) {
+    cost[0] = shape_cost(M, N, 64, 64, 60, 80);
+    cost[1] = shape_cost(M, N, 128, 64, 79, 127);
+    cost[2] = shape_cost(M, N, 128, 128, 126, 206);
+  } else {
+    cost[0] = shape_cost(M, N, 64, 64, 36, 55);
+    cost[1] = shape_cost(M, N, 128, 64, 49, 75);
+    cost[2] = shape_cost(M, N, 128, 128, 90, 122);
+    cost[3] = shape_cost(M, N, 128, 256, 118, 236);
+    cost[4] = shape_cost(M, N, 256, 256, 170, 340);
+  }
+  int best = 0;
+  for (int i = 1; i < kShapes; ++i)
+    if (cost[i] < cost[best]) best = i;
+  if constexpr (!WIDE) {
+    if (best == 4) return dense<S256x256, BROWS, WIDE>(M, N, K, a, b, y, stream);
+    if (best == 3) return dense<S128x256, BROWS, WIDE>(M, N, K, a, b, y, stream);
+  }
+  if (best == 2) return dense<S128x128, BROWS, WIDE>(M, N, K, a, b, y, stream);
+  if (best == 1) return dense<S128x64, BROWS, WIDE>(M, N, K, a, b, y, stream);
+  return dense<S64x64, BROWS, WIDE>(M, N, K, a, b, y, stream);
+}
+
+template <typename S, bool GATHER, bool WIDE>
 hipError_t grouped(int32_t G, const int32_t* m_offsets, const int32_t* row_index, int64_t total_m,
                    int64_t a_rows, int64_t N, int64_t K, Fp8Operand a, Fp8Operand b, Fp8Out y,
                    hipStream_t stream) {
-  constexpr int BM = 64, BN = 128, S = 2;
-  using T = Tile<BM, BN, 2, 2, S, false, WIDE>;
-  auto kern = fp8_grouped_kernel<BM, BN, 2, 2, S, GATHER, WIDE>;
+  using T = Tile<S::BM, S::BN, S::WM, S::WN, S::S, false, WIDE>;
+  auto kern = fp8_grouped_kernel<S::BM, S::BN, S::WM, S::WN, S::S, GATHER, WIDE>;
   static std::atomic<uint64_t> done{0};
   const hipError_t err = allow_lds(kern, T::kSmem, done);
   if (err != hipSuccess) return err;
-  kern<<<768, T::kThreads, T::kSmem, stream>>>(G, m_offsets, row_index, total_m, a_rows, N, K, a, b, y);
+  constexpr unsigned per_cu = T::kSmem > 80 * 1024 ? 1 : 2;
+  kern<<<256 * per_cu, T::kThreads, T::kSmem, stream>>>(G, m_offsets, row_index, total_m, a_rows, N,
+                                                        K, a, b, y);
   return hipGetLastError();
 }
 
-template <bool WIDE>
+template <bool GATHER, bool WIDE>
+hipError_t grouped_any(int32_t G, const int32_t* m_offsets, const int32_t* row_index,
+                       int64_t total_m, int64_t a_rows, int64_t N, int64_t K, Fp8Operand a,
+                       Fp8Operand b, Fp8Out y, hipStream_t stream) {
+  // the counts are on the device: the shape goes by the mean
+  const int64_t mean = total_m / G;
+  if constexpr (!WIDE) {
+    if (mean > 128)
+      return grouped<S256x256, GATHER, WIDE>(G, m_offsets, row_index, total_m, a_rows, N, K, a, b, y, stream);
+  }
+  if (mean > 64)
+    return grouped<S128x128, GATHER, WIDE>(G, m_offsets, row_index, total_m, a_rows, N, K, a, b, y, stream);
+  return grouped<S64x128, GATHER, WIDE>(G, m_offsets, row_index, total_m, a_rows, N, K, a, b, y, stream);
+}
+
+template <typename S, bool WIDE>
 hipError_t wgrad(int32_t G, const int32_t* m_offsets, int64_t total_m, int64_t P, int64_t N,
                  int64_t K, Fp8Operand a, Fp8Operand b, Fp8Out y, hipStream_t stream) {
-  constexpr int BM = 128, BN = 128, S = 2;
-  using T = Tile<BM, BN, 2, 2, S, true, WIDE>;
-  auto kern = fp8_wgrad_kernel<BM, BN, 2, 2, S, WIDE>;
+  using T = Tile<S::BM, S::BN, S::WM, S::WN, S::S, true, WIDE>;
+  auto kern = fp8_wgrad_kernel<S::BM, S::BN, S::WM, S::WN, S::S, WIDE>;
   static std::atomic<uint64_t> done{0};
   const hipError_t err = allow_lds(kern, T::kSmem, done);
   if (err != hipSuccess) return err;
-  const int64_t tiles = (int64_t)G * ((N + BM - 1) / BM) * ((K + BN - 1) / BN);
+  const int64_t tiles = (int64_t)G * ((N + S::BM - 1) / S::BM) * ((K + S::BN - 1) / S::BN);
   if (tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
   kern<<<(unsigned)tiles, T::kThreads, T::kSmem, stream>>>(G, m_offsets, total_m, P, N, K, a, b, y);
   return hipGetLastError();
@@ -200,10 +271,14 @@ hipError_t by_width(const Fp8Out& y, F&& f) {
 
 hipError_t launch_fp8_gemm(int64_t M, int64_t N, int64_t K, Fp8Operand a, Fp8Operand b,
                            int b_block_rows, Fp8Out y, hipStream_t stream) {
+  // up to 32 rows the weights' stream is all that counts (M = 32, N = K =
+  // 8192: 21 us streamed, 31 in 64 x 64 tiles; from 33 rows on the stream
+  // kernel re-reads A too often: M = 64 29 us, tiles 23)
+  if (M <= 32) return launch_fp8_stream(M, N, K, a, b, b_block_rows, y, stream);
   return by_width(y, [&](auto wide) {
     constexpr bool W = decltype(wide)::value;
-    return b_block_rows == 1 ? dense<true, W>(M, N, K, a, b, y, stream)
-                             : dense<false, W>(M, N, K, a, b, y, stream);
+    return b_block_rows == 1 ? dense_any<true, W>(M, N, K, a, b, y, stream)
+                             : dense_any<false, W>(M, N, K, a, b, y, stream);
   });
 }
 
@@ -213,17 +288,16 @@ hipError_t launch_fp8_grouped(int32_t G, const int32_t* m_offsets, const int32_t
   return by_width(y, [&](auto wide) {
     constexpr bool W = decltype(wide)::value;
     return row_index != nullptr
-               ? grouped<true, W>(G, m_offsets, row_index, total_m, a_rows, N, K, a, b, y, stream)
-               : grouped<false, W>(G, m_offsets, row_index, total_m, a_rows, N, K, a, b, y, stream);
+               ? grouped_any<true, W>(G, m_offsets, row_index, total_m, a_rows, N, K, a, b, y, stream)
+               : grouped_any<false, W>(G, m_offsets, row_index, total_m, a_rows, N, K, a, b, y, stream);
   });
 }
 
 hipError_t launch_fp8_wgrad(int32_t G, const int32_t* m_offsets, int64_t total_m, int64_t P,
                             int64_t N, int64_t K, Fp8Operand a, Fp8Operand b, Fp8Out y,
                             hipStream_t stream) {
-  return by_width(y, [&](auto wide) {
-    return wgrad<decltype(wide)::value>(G, m_offsets, total_m, P, N, K, a, b, y, stream);
-  });
+  if (y.dtype == 0) return wgrad<S128x128, true>(G, m_offsets, total_m, P, N, K, a, b, y, stream);
+  return wgrad<S256x256, false>(G, m_offsets, total_m, P, N, K, a, b, y, stream);
 }
 
 }  // namespace nvfp4

@@ -55,209 +55,8 @@ struct TileOut {
   bool vec;       // rows are 16-byte aligned
 };
 
-template <int BM, int BN, int WM, int WN, int STAGES, bool BROWS, bool WIDE>
-struct Tile {
-  static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
-  static constexpr int TM = BM / WM, TN = BN / WN;
-  static constexpr int FM = TM / 16, FN = TN / 16;
-  static constexpr int kALoads = BM / 8 / kWaves, kBLoads = BN / 8 / kWaves;
-  static constexpr int kScales = (BM + BN) / 64;  // scale-load instructions of a stage
-  static constexpr int kSLoads = (kScales + kWaves - 1) / kWaves;
-  static constexpr int kLoads = kALoads + kBLoads + kSLoads;  // per wave and stage
-  static constexpr int kAOff = 0, kBOff = BM * kBlock, kSOff = (BM + BN) * kBlock;
-  static constexpr int kStage = kSOff + (BM + BN) * 4;
-  static constexpr int kSmem = STAGES * kStage;
-  static_assert(BM % (8 * kWaves) == 0 && BN % (8 * kWaves) == 0, "whole loads per wave");
-  static_assert(BM % 64 == 0 && BN % 64 == 0 && TN % 32 == 0 && TM % 16 == 0, "fragment shapes");
-  static_assert(BROWS || 128 % TN == 0, "one weight scale per wave and block");
-  static_assert((STAGES - 2) * kLoads < 64, "vmcnt range");
-
-  // 16 lanes of an activation fragment read rows r .. r + 15: two rows share
-  // a 256-byte bank line, so the chunk moves with row / 2.
-  static __device__ __forceinline__ int swz_a(int r) { return (r >> 1) & 7; }
-  // 16 lanes of a weight fragment read rows 8 * (l / 4) + l % 4 (+ 4): the
-  // chunk moves with row bits 1, 3 and 4.
-  static __device__ __forceinline__ int swz_b(int r) { return ((r >> 1) & 1) | ((r >> 2) & 6); }
-
-  // K: elements of the sum; ld: bytes between rows of both operands.
-  template <bool GATHER>
-  static __device__ __forceinline__ void run(const TileOperand& A, const TileOperand& B, uint32_t K,
-                                             uint32_t ld, const TileOut& out, uint8_t* smem) {
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave / WN, wn = wave % WN;
-    const int li = lane & 15, lg = lane >> 4;
-    const int nk = (int)((K + kBlock - 1) / kBlock);
-
-    uint32_t a_off[kALoads], b_off[kBLoads], s_off[kSLoads];
-    uint32_t a_chunk[kALoads], b_chunk[kBLoads];
-#pragma unroll
-    for (int i = 0; i < kALoads; ++i) {
-      const int r = (wave * kALoads + i) * 8 + (lane >> 3);
-      a_chunk[i] = (uint32_t)(((lane & 7) ^ swz_a(r)) << 4);
-      uint32_t row = (uint32_t)r;
-      bool ok = true;
-      if constexpr (GATHER) {
-        const int32_t v = r < A.index_n ? A.index[r] : -1;
-        ok = v >= 0 && v < A.index_max;
-        row = (uint32_t)v;
-      }
-      a_off[i] = ok ? row * ld + a_chunk[i] : kNoRow;
-    }
-#pragma unroll
-    for (int i = 0; i < kBLoads; ++i) {
-      const int r = (wave * kBLoads + i) * 8 + (lane >> 3);
-      b_chunk[i] = (uint32_t)(((lane & 7) ^ swz_b(r)) << 4);
-      b_off[i] = (uint32_t)r * ld + b_chunk[i];
-    }
-    // scale loads: instruction j < BM / 64 takes the activations' rows, the
-    // others the weights'; waves past the last repeat one (same bytes, same
-    // place), so every wave issues the same number of loads
-    bool s_is_a[kSLoads];
-    int s_slot[kSLoads];
-#pragma unroll
-    for (int i = 0; i < kSLoads; ++i) {
-      const int j = (wave * kSLoads + i) % kScales;
-      s_slot[i] = j;
-      s_is_a[i] = j < BM / 64;
-      const int r = (s_is_a[i] ? j : j - BM / 64) * 64 + lane;
-      if (s_is_a[i]) {
-        uint32_t row = (uint32_t)r;
-        bool ok = true;
-        if constexpr (GATHER) {
-          const int32_t v = r < A.index_n ? A.index[r] : -1;
-          ok = v >= 0 && v < A.index_max;
-          row = (uint32_t)v;
-        }
-        s_off[i] = ok ? row * 4 : kNoRow;
-      } else {
-        s_off[i] = (uint32_t)(BROWS ? r : r / kBlock) * 4;
-      }
-    }
-
-    // the loads of stage s into ring slot `slot`; past the last stage every
-    // lane is out of range (zeros into a slot that is not read again)
-    auto issue = [&](int s, int slot) {
-      uint8_t* base = smem + slot * kStage;
-      const bool live = s < nk;
-      const uint32_t soff = (uint32_t)s * kBlock;
-      const auto ra = make_rsrc(A.q, live ? A.q_bytes : 0u);
-      const auto rb = make_rsrc(B.q, live ? B.q_bytes : 0u);
-      const uint32_t left = K - soff;  // bytes of K from this stage on
-      if (left >= kBlock || !live) {
-#pragma unroll
-        for (int i = 0; i < kALoads; ++i)
-          load_lds16(ra, base + kAOff + (wave * kALoads + i) * 1024, a_off[i], soff);
-#pragma unroll
-        for (int i = 0; i < kBLoads; ++i)
-          load_lds16(rb, base + kBOff + (wave * kBLoads + i) * 1024, b_off[i], soff);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kALoads; ++i)
-          load_lds16(ra, base + kAOff + (wave * kALoads + i) * 1024,
-                     a_chunk[i] < left ? a_off[i] : kNoRow, soff);
-#pragma unroll
-        for (int i = 0; i < kBLoads; ++i)
-          load_lds16(rb, base + kBOff + (wave * kBLoads + i) * 1024,
-                     b_chunk[i] < left ? b_off[i] : kNoRow, soff);
-      }
-#pragma unroll
-      for (int i = 0; i < kSLoads; ++i) {
-        const TileOperand& o = s_is_a[i] ? A : B;
-        load_lds4(make_rsrc(o.s + (live ? s * o.s_ld : 0), live ? o.s_bytes : 0u),
-                  base + kSOff + s_slot[i] * 256, s_off[i], 0);
-      }
-    };
-
-    f32x4 acc[FN][FM];
-#pragma unroll
-    for (int i = 0; i < FN; ++i)
-#pragma unroll
-      for (int j = 0; j < FM; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-    // LDS addresses of the fragments: a lane takes chunks lg and lg + 4 of
-    // its row in both operands
-    const int b_row0 = wn * TN + 8 * (li >> 2) + (li & 3);
-    auto read_b = [&](const uint8_t* st, int i) {
-      const int r = b_row0 + 32 * (i >> 1) + 4 * (i & 1);
-      const uint8_t* p = st + kBOff + r * kBlock;
-      const int sw = swz_b(r);
-      return join(*reinterpret_cast<const u32x4*>(p + ((lg ^ sw) << 4)),
-                  *reinterpret_cast<const u32x4*>(p + (((lg + 4) ^ sw) << 4)));
-    };
-    auto read_a = [&](const uint8_t* st, int j) {
-      const int r = wm * TM + 16 * j + li;
-      const uint8_t* p = st + kAOff + r * kBlock;
-      const int sw = swz_a(r);
-      return join(*reinterpret_cast<const u32x4*>(p + ((lg ^ sw) << 4)),
-                  *reinterpret_cast<const u32x4*>(p + (((lg + 4) ^ sw) << 4)));
-    };
-
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) issue(s, s);
-    int slot = 0;
-    for (int s = 0; s < nk; ++s) {
-      wait_vmcnt<(STAGES - 2) * kLoads>();
-      workgroup_barrier();
-      // every wave is past stage s - 1: its slot takes stage s + STAGES - 1
-      issue(s + STAGES - 1, slot == 0 ? STAGES - 1 : slot - 1);
-      const uint8_t* st = smem + slot * kStage;
-      const float* sc = reinterpret_cast<const float*>(st + kSOff);
-      decltype(fragment<WIDE>(i32x8{})) bf[FN];
-#pragma unroll
-      for (int i = 0; i < FN; ++i) bf[i] = fragment<WIDE>(read_b(st, i));
-      float fa[FM];
-#pragma unroll
-      for (int j = 0; j < FM; ++j) fa[j] = sc[wm * TM + 16 * j + li];
-      f32x4 fb[BROWS ? FN : 1];
-      if constexpr (BROWS) {
-#pragma unroll
-        for (int i = 0; i < FN; ++i)
-          fb[i] = *reinterpret_cast<const f32x4*>(sc + BM + wn * TN + 32 * (i >> 1) + 8 * lg + 4 * (i & 1));
-      } else {
-        const float f = sc[BM + wn * TN];
-#pragma unroll
-        for (int j = 0; j < FM; ++j) fa[j] *= f;
-      }
-#pragma unroll
-      for (int j = 0; j < FM; ++j) {
-        const auto af = fragment<WIDE>(read_a(st, j));
-#pragma unroll
-        for (int i = 0; i < FN; ++i) {
-          const f32x4 c = mfma_block(bf[i], af);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float f = BROWS ? fb[BROWS ? i : 0][e] * fa[j] : fa[j];
-            acc[i][j][e] = __builtin_fmaf(c[e], f, acc[i][j][e]);
-          }
-        }
-      }
-      slot = slot + 1 == STAGES ? 0 : slot + 1;
-    }
-    // the ring's last loads land before the slots can be written again
-    wait_vmcnt<0>();
-
-#pragma unroll
-    for (int j = 0; j < FM; ++j) {
-      const int m = wm * TM + 16 * j + li;
-      if (m >= out.m) continue;
-#pragma unroll
-      for (int p = 0; p < FN / 2; ++p) {
-        const int n = wn * TN + 32 * p + 8 * lg;
-        if (n >= out.n) continue;
-        float v[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[e] = acc[2 * p][j][e];
-          v[4 + e] = acc[2 * p + 1][j][e];
-        }
-        store8(out, m, n, v);
-      }
-    }
-  }
-
   // Eight neighbouring outputs of one row (those below out.n).
-  static __device__ __forceinline__ void store8(const TileOut& out, int m, int n, const float* v) {
+  __device__ __forceinline__ void store8(const TileOut& out, int m, int n, const float* v) {
     const int64_t at = (int64_t)m * out.ld + n;
     if (out.vec && n + 8 <= out.n) {
       if (out.dtype == 1) {
@@ -288,6 +87,275 @@ struct Tile {
             *p = out.add ? *p + v[e] : v[e];
           }
         }
+    }
+  }
+
+template <int BM, int BN, int WM, int WN, int STAGES, bool BROWS, bool WIDE>
+struct Tile {
+  static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+  static constexpr int TM = BM / WM, TN = BN / WN;
+  static constexpr int FM = TM / 16, FN = TN / 16;
+  static constexpr int kALoads = BM / 8 / kWaves, kBLoads = BN / 8 / kWaves;
+  static constexpr int kScales = (BM + BN) / 64;  // scale-load instructions of a stage
+  static constexpr int kSLoads = (kScales + kWaves - 1) / kWaves;
+  static constexpr int kLoads = kALoads + kBLoads + kSLoads;  // per wave and stage
+  static constexpr int kAOff = 0, kBOff = BM * kBlock, kSOff = (BM + BN) * kBlock;
+  static constexpr int kStage = kSOff + (BM + BN) * 4;
+  static constexpr int kSmem = STAGES * kStage;
+  static_assert(BM % (8 * kWaves) == 0 && BN % (8 * kWaves) == 0, "whole loads per wave");
+  static_assert((kALoads & (kALoads - 1)) == 0 && (kBLoads & (kBLoads - 1)) == 0,
+                "the loads' row bits are disjoint");
+  static_assert(BM % 64 == 0 && BN % 64 == 0 && TN % 32 == 0 && TM % 16 == 0, "fragment shapes");
+  static_assert(BROWS || 128 % TN == 0, "one weight scale per wave and block");
+  static_assert(FM % 2 == 0 && FN >= 2, "pairs of fragments");
+  static_assert((STAGES - 1) * kLoads < 64, "vmcnt range");
+
+  // 16 lanes of an activation fragment read rows r .. r + 15: two rows share
+  // a 256-byte bank line, so the chunk moves with row / 2.
+  static __device__ __forceinline__ int swz_a(int r) { return (r >> 1) & 7; }
+  // 16 lanes of a weight fragment read rows 8 * (l / 4) + l % 4 (+ 4): the
+  // chunk moves with row bits 1, 3 and 4.
+  static __device__ __forceinline__ int swz_b(int r) { return ((r >> 1) & 1) | ((r >> 2) & 6); }
+
+  // K: elements of the sum; ld: bytes between rows of both operands.
+  template <bool GATHER>
+  static __device__ __forceinline__ void run(const TileOperand& A, const TileOperand& B, uint32_t K,
+                                             uint32_t ld, const TileOut& out, uint8_t* smem) {
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    const int li = lane & 15, lg = lane >> 4;
+    const int nk = (int)((K + kBlock - 1) / kBlock);
+
+    uint32_t a_off[kALoads], b_off[kBLoads], s_off[kSLoads];
+    // a load's 16-byte chunk of its rows; rows 8 apart only flip fixed bits
+    const int lr = lane >> 3;
+    const uint32_t a_chunk = (uint32_t)(((lane & 7) ^ swz_a(wave * kALoads * 8 + lr)) << 4);
+    const uint32_t b_chunk = (uint32_t)(((lane & 7) ^ swz_b(wave * kBLoads * 8 + lr)) << 4);
+#pragma unroll
+    for (int i = 0; i < kALoads; ++i) {
+      const int r = (wave * kALoads + i) * 8 + (lane >> 3);
+      uint32_t row = (uint32_t)r;
+      bool ok = true;
+      if constexpr (GATHER) {
+        const int32_t v = r < A.index_n ? A.index[r] : -1;
+        ok = v >= 0 && v < A.index_max;
+        row = (uint32_t)v;
+      }
+      a_off[i] = ok ? row * ld + (a_chunk ^ (swz_a(i * 8) << 4)) : kNoRow;
+    }
+#pragma unroll
+    for (int i = 0; i < kBLoads; ++i) {
+      const int r = (wave * kBLoads + i) * 8 + (lane >> 3);
+      b_off[i] = (uint32_t)r * ld + (b_chunk ^ (swz_b(i * 8) << 4));
+    }
+    // chunks of the last block that lie past K: lane masks in scalar
+    // registers, so a stage's loads need no branch (one would let the
+    // compiler move the products' additions across it)
+    const uint32_t end = K - (uint32_t)(nk - 1) * kBlock;
+    bool a_past[kALoads], b_past[kBLoads];
+#pragma unroll
+    for (int i = 0; i < kALoads; ++i) a_past[i] = (a_chunk ^ (uint32_t)(swz_a(i * 8) << 4)) >= end;
+#pragma unroll
+    for (int i = 0; i < kBLoads; ++i) b_past[i] = (b_chunk ^ (uint32_t)(swz_b(i * 8) << 4)) >= end;
+    // scale loads: instruction j < BM / 64 takes the activations' rows, the
+    // others the weights'; waves past the last repeat one (same bytes, same
+    // place), so every wave issues the same number of loads
+    bool s_is_a[kSLoads];
+    int s_slot[kSLoads];
+#pragma unroll
+    for (int i = 0; i < kSLoads; ++i) {
+      const int j = (wave * kSLoads + i) % kScales;
+      s_slot[i] = j;
+      s_is_a[i] = j < BM / 64;
+      const int r = (s_is_a[i] ? j : j - BM / 64) * 64 + lane;
+      if (s_is_a[i]) {
+        uint32_t row = (uint32_t)r;
+        bool ok = true;
+        if constexpr (GATHER) {
+          const int32_t v = r < A.index_n ? A.index[r] : -1;
+          ok = v >= 0 && v < A.index_max;
+          row = (uint32_t)v;
+        }
+        s_off[i] = ok ? row * 4 : kNoRow;
+      } else {
+        s_off[i] = (uint32_t)(BROWS ? r : r / kBlock) * 4;
+      }
+    }
+
+    // load number J (0 .. kLoads - 1) of stage s into ring slot `slot`; past
+    // the last stage every lane is out of range (zeros into a slot that is
+    // not read again)
+    auto load_one = [&](int s, int slot, auto jc) {
+      constexpr int J = decltype(jc)::value;
+      uint8_t* base = smem + slot * kStage;
+      const bool live = s < nk, cut = s == nk - 1;
+      const uint32_t soff = (uint32_t)s * kBlock;
+      if constexpr (J < kBLoads) {
+        constexpr int i = J;
+        load_lds16(make_rsrc(B.q, live ? B.q_bytes : 0u), base + kBOff + (wave * kBLoads + i) * 1024,
+                   cut && b_past[i] ? kNoRow : b_off[i], soff);
+      } else if constexpr (J < kBLoads + kALoads) {
+        constexpr int i = J - kBLoads;
+        load_lds16(make_rsrc(A.q, live ? A.q_bytes : 0u), base + kAOff + (wave * kALoads + i) * 1024,
+                   cut && a_past[i] ? kNoRow : a_off[i], soff);
+      } else {
+        constexpr int i = J - kBLoads - kALoads;
+        const float* p = s_is_a[i] ? A.s : B.s;
+        const int64_t at = (int64_t)max(min(s, nk - 1), 0) * (s_is_a[i] ? A.s_ld : B.s_ld);
+        const uint32_t bytes = s_is_a[i] ? A.s_bytes : B.s_bytes;
+        load_lds4(make_rsrc(p + at, live ? bytes : 0u), base + kSOff + s_slot[i] * 256, s_off[i], 0);
+      }
+    };
+    auto issue = [&](int s, int slot, auto n) {
+      static_for<decltype(n)::value>([&](auto jc) { load_one(s, slot, jc); });
+    };
+
+    f32x4 acc[FN][FM];
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+      for (int j = 0; j < FM; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    // fragments: a lane takes chunks lg and lg + 4 of its row in both
+    // operands (the swizzles do not depend on the fragment's number)
+    const int b_row0 = wn * TN + 8 * (li >> 2) + (li & 3), a_row0 = wm * TM + li;
+    const int b_sw = swz_b(b_row0), a_sw = swz_a(a_row0);
+    const int b_at = kBOff + b_row0 * kBlock, a_at = kAOff + a_row0 * kBlock;
+    auto read = [&](const uint8_t* p, int sw) {
+      return join(*reinterpret_cast<const u32x4*>(p + ((lg ^ sw) << 4)),
+                  *reinterpret_cast<const u32x4*>(p + (((lg + 4) ^ sw) << 4)));
+    };
+    auto read_b = [&](const uint8_t* st, int i) {
+      return read(st + b_at + (32 * (i >> 1) + 4 * (i & 1)) * kBlock, b_sw);
+    };
+    auto read_a = [&](const uint8_t* st, int j) { return read(st + a_at + 16 * j * kBlock, a_sw); };
+    auto scales = [&](const uint8_t* st) { return reinterpret_cast<const float*>(st + kSOff); };
+
+    // The loop works on pairs of activation fragments: a pair meets all FN
+    // weight fragments while the next pair is read.  In a stage's last pair
+    // the workgroup meets (the next stage has landed, this one has been read
+    // by all), its slot is refilled and the next stage's first pair and
+    // weight fragments are read, each into the registers of the fragment just
+    // used -- so the matrix core does not wait for LDS at a stage's start.
+    // The refill goes out one load at a time over the Q / 2 products from the
+    // meeting on (into the next stage): a wave that issues all of them at
+    // once waits for the address unit with its products behind it.
+    // A product's result is added two products later, when it is ready.
+    using Frag = decltype(fragment<WIDE>(i32x8{}));
+    constexpr int PAIRS = FM / 2, PER = 2 * FN, Q = PAIRS * PER;
+    i32x8 br[FN], ar[2];
+    float fw = 1.f;
+    f32x4 fb[BROWS ? FN : 1];
+    f32x4 cq[3];
+    Frag bw[FN], aw[2];
+
+    constexpr int MEET = (PAIRS - 1) * PER, SPREAD = Q / 2;
+    constexpr int EARLY = ((Q - MEET) * kLoads + SPREAD - 1) / SPREAD < kLoads
+                              ? ((Q - MEET) * kLoads + SPREAD - 1) / SPREAD
+                              : kLoads;  // loads that go out in the stage of the meeting
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) issue(s, s, std::integral_constant<int, kLoads>{});
+    issue(STAGES - 1, STAGES - 1, std::integral_constant<int, EARLY>{});
+    wait_vmcnt<(STAGES - 2) * kLoads + EARLY>();
+    workgroup_barrier();
+#pragma unroll
+    for (int i = 0; i < FN; ++i) br[i] = read_b(smem, i);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) ar[h] = read_a(smem, h);
+    int slot = 0;
+    for (int s = 0; s < nk; ++s) {
+      const uint8_t* st = smem + slot * kStage;
+      const int next = slot + 1 == STAGES ? 0 : slot + 1;
+      const uint8_t* nst = smem + next * kStage;
+      const float* sc = scales(st);
+      if constexpr (BROWS) {
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+          fb[i] = *reinterpret_cast<const f32x4*>(sc + BM + wn * TN + 32 * (i >> 1) + 8 * lg + 4 * (i & 1));
+      } else {
+        fw = sc[BM + wn * TN];
+      }
+      float fall[FM];
+#pragma unroll
+      for (int j = 0; j < FM; ++j) fall[j] = sc[a_row0 + 16 * j];
+      i32x8 an[2];
+      auto add = [&](auto qc) {
+        constexpr int q = decltype(qc)::value, p = q / PER, i = (q % PER) / 2, h = q % 2, j = 2 * p + h;
+        const f32x4& c = cq[q % 3];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float f = BROWS ? fb[BROWS ? i : 0][e] * fall[j] : fall[j];
+          acc[i][j][e] = __builtin_fmaf(c[e], f, acc[i][j][e]);
+        }
+      };
+      static_for<Q>([&](auto qc) {
+        constexpr int q = decltype(qc)::value, p = q / PER, r = q % PER, i = r / 2, h = r % 2;
+        constexpr bool last = p == PAIRS - 1;
+        if constexpr (r == 0) {
+          if constexpr (last) {
+            // this wave's reads of the stage are done, its loads of the next
+            // one have landed
+            wait_lgkmcnt0();
+            wait_vmcnt<(STAGES - 2) * kLoads>();
+          }
+          aw[0] = fragment<WIDE>(ar[0]);
+          aw[1] = fragment<WIDE>(ar[1]);
+        }
+        if constexpr (p == 0 && h == 0) bw[i] = fragment<WIDE>(br[i]);
+        if constexpr (p == 0 && r == 0 && !BROWS) {
+#pragma unroll
+          for (int j = 0; j < FM; ++j) fall[j] *= fw;
+        }
+        cq[q % 3] = mfma_block(bw[i], aw[h]);
+        if constexpr (q >= 2) add(std::integral_constant<int, q - 2>{});
+        if constexpr (last && r == 0) workgroup_barrier();
+        // refill: load n at MEET + n * SPREAD / kLoads, counted on into the
+        // next stage
+        static_for<kLoads>([&](auto nc) {
+          constexpr int n = decltype(nc)::value, at = MEET + n * SPREAD / kLoads;
+          if constexpr (at == q) load_one(s + STAGES, slot, nc);
+          if constexpr (at - Q == q) load_one(s + STAGES - 1, slot == 0 ? STAGES - 1 : slot - 1, nc);
+        });
+        // the next pair (of this stage or the next), then the next stage's
+        // weights behind their last use
+        if constexpr (!last) {
+          if constexpr (r == 0) an[0] = read_a(st, 2 * p + 2);
+          if constexpr (r == 1) an[1] = read_a(st, 2 * p + 3);
+        } else {
+          if constexpr (r == 1) an[0] = read_a(nst, 0);
+          if constexpr (r == 3) an[1] = read_a(nst, 1);
+          if constexpr (h == 1) br[i] = read_b(nst, i);
+        }
+        if constexpr (r == PER - 1) {
+          ar[0] = an[0];
+          ar[1] = an[1];
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      });
+      add(std::integral_constant<int, Q - 2>{});
+      add(std::integral_constant<int, Q - 1>{});
+      slot = next;
+    }
+    // the ring's last loads land before the slots can be written again
+    wait_vmcnt<0>();
+
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      const int m = wm * TM + 16 * j + li;
+      if (m >= out.m) continue;
+#pragma unroll
+      for (int p = 0; p < FN / 2; ++p) {
+        const int n = wn * TN + 32 * p + 8 * lg;
+        if (n >= out.n) continue;
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] = acc[2 * p][j][e];
+          v[4 + e] = acc[2 * p + 1][j][e];
+        }
+        store8(out, m, n, v);
+      }
     }
   }
 };
