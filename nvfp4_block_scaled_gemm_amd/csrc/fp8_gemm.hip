@@ -114,8 +114,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_wgrad_kernel(
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   using T = Tile<BM, BN, WM, WN, STAGES, true, WIDE>;
   const int tiles_m = (int)ceil_div(N, BM), tiles_n = (int)ceil_div(K, BN);
-  const int pid = xcd_run(blockIdx.x, gridDim.x);
-  const int e = pid / (tiles_m * tiles_n), in = pid % (tiles_m * tiles_n);
+  // every XCD takes an eighth of each expert's tiles, so that experts of
+  // uneven load keep them all busy
+  const int tiles = tiles_m * tiles_n, per = (tiles + kXcds - 1) / kXcds;
+  const int e = blockIdx.x / kXcds / per, in = blockIdx.x % kXcds * per + blockIdx.x / kXcds % per;
+  if (in >= tiles) return;
   const int64_t m0 = (int64_t)(in % tiles_m) * BM, n0 = (int64_t)(in / tiles_m) * BN;
   const int lane = threadIdx.x & 63;
   uint32_t blocks = 0;  // blocks of the experts before e
@@ -254,9 +257,10 @@ hipError_t wgrad(int32_t G, const int32_t* m_offsets, int64_t total_m, int64_t P
   static std::atomic<uint64_t> done{0};
   const hipError_t err = allow_lds(kern, T::kSmem, done);
   if (err != hipSuccess) return err;
-  const int64_t tiles = (int64_t)G * ((N + S::BM - 1) / S::BM) * ((K + S::BN - 1) / S::BN);
-  if (tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
-  kern<<<(unsigned)tiles, T::kThreads, T::kSmem, stream>>>(G, m_offsets, total_m, P, N, K, a, b, y);
+  const int64_t tiles = ((N + S::BM - 1) / S::BM) * ((K + S::BN - 1) / S::BN);
+  const int64_t grid = G * ((tiles + kXcds - 1) / kXcds) * kXcds;
+  if (tiles > 0x7FFFFFFF || grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+  kern<<<(unsigned)grid, T::kThreads, T::kSmem, stream>>>(G, m_offsets, total_m, P, N, K, a, b, y);
   return hipGetLastError();
 }
 

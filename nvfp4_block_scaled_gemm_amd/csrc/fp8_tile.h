@@ -340,21 +340,70 @@ struct Tile {
     // the ring's last loads land before the slots can be written again
     wait_vmcnt<0>();
 
+    // The wave's tile goes out through its own part of the idle ring, in
+    // passes of 32 rows: lanes write what they hold, then read whole row
+    // pieces, so that a store covers runs of TN elements instead of four.
+    // (LDS accesses of one wave complete in order.)
+    workgroup_barrier();
+    constexpr int RS = TN + 4;  // floats per staged row; + 4 spreads the banks
+    static_assert(kWaves * 32 * RS * 4 <= kSmem, "staging fits the ring");
+    float* stage = reinterpret_cast<float*>(smem) + wave * 32 * RS;
+    constexpr int LPR = TN / 8, RPI = 64 / LPR;  // lanes per row, rows per read
+    constexpr int NP = 32 / RPI;
+    // whole rows of fp32: two runs of 16 bytes per lane, TN / 2 columns apart.
+    // What they add to is read ahead of everything, in one go.
+    const bool runs = WIDE && out.vec && (wn + 1) * TN <= out.n;
+    float* const y32 = reinterpret_cast<float*>(out.y) + wn * TN + 4 * (lane % LPR);
+    f32x4 old[WIDE ? FM / 2 : 1][WIDE ? NP : 1][2];
+    if constexpr (WIDE) {
+      if (runs && out.add) {
 #pragma unroll
-    for (int j = 0; j < FM; ++j) {
-      const int m = wm * TM + 16 * j + li;
-      if (m >= out.m) continue;
+        for (int j2 = 0; j2 < FM / 2; ++j2)
 #pragma unroll
-      for (int p = 0; p < FN / 2; ++p) {
-        const int n = wn * TN + 32 * p + 8 * lg;
-        if (n >= out.n) continue;
-        float v[8];
+          for (int p = 0; p < NP; ++p) {
+            const int m = min(wm * TM + 32 * j2 + p * RPI + lane / LPR, out.m - 1);
+            const float* y = y32 + (int64_t)m * out.ld;
+            old[j2][p][0] = *reinterpret_cast<const f32x4*>(y);
+            old[j2][p][1] = *reinterpret_cast<const f32x4*>(y + TN / 2);
+          }
+      } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[e] = acc[2 * p][j][e];
-          v[4 + e] = acc[2 * p + 1][j][e];
+        for (int j2 = 0; j2 < FM / 2; ++j2)
+#pragma unroll
+          for (int p = 0; p < NP; ++p) old[j2][p][0] = old[j2][p][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+    }
+#pragma unroll
+    for (int j2 = 0; j2 < FM / 2; ++j2) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+          *reinterpret_cast<f32x4*>(stage + (16 * h + li) * RS + 32 * (i >> 1) + 8 * lg + 4 * (i & 1)) = acc[i][2 * j2 + h];
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        const int r = p * RPI + lane / LPR;
+        const int m = wm * TM + 32 * j2 + r, c = lane % LPR;
+        bool done = false;
+        if constexpr (WIDE) {
+          if (runs) {
+            const f32x4 lo = *reinterpret_cast<const f32x4*>(stage + r * RS + 4 * c);
+            const f32x4 hi = *reinterpret_cast<const f32x4*>(stage + r * RS + TN / 2 + 4 * c);
+            if (m < out.m) {
+              float* y = y32 + (int64_t)m * out.ld;
+              *reinterpret_cast<f32x4*>(y) = lo + old[j2][p][0];
+              *reinterpret_cast<f32x4*>(y + TN / 2) = hi + old[j2][p][1];
+            }
+            done = true;
+          }
         }
-        store8(out, m, n, v);
+        if (!done) {
+          const int n = wn * TN + 8 * c;
+          const f32x4 lo = *reinterpret_cast<const f32x4*>(stage + r * RS + 8 * c);
+          const f32x4 hi = *reinterpret_cast<const f32x4*>(stage + r * RS + 8 * c + 4);
+          const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+          if (m < out.m && n < out.n) store8(out, m, n, v);
+        }
       }
     }
   }
