@@ -530,9 +530,22 @@ def nvfp4_mxfp4_gemm(a, b, out_dtype: str = "bf16", y: torch.Tensor | None = Non
 _F8 = torch.float8_e4m3fn
 
 
-def _on_gpu(dev: int):
-    """Context in which the library launches on GPU ``dev``."""
-    return contextlib.nullcontext() if torch.cuda.current_device() == dev else torch.cuda.device(dev)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+@contextlib.contextmanager
+def _there(stream, dev: int):
+    """Context for a call on another stream than the current one, or on
+    another GPU than the current one."""
+    with torch.cuda.device(dev), _on_stream(stream, dev):
+        yield
+
+
+def _here(stream, dev: int) -> bool:
+    """Whether a call runs on the current stream of the current GPU and needs
+    no context (the usual case, kept cheap: a context costs about as much as
+    a launch)."""
+    return stream is None and _current_device() == dev
 
 
 def _stride(t, cols: int, what: str) -> int:
@@ -548,16 +561,21 @@ class Fp8Packed(tuple):
     contiguous, on one GPU; block_rows is 1 or 128, told by s's shape.
     Checked when made; nvfp4_fp8_quantize returns one."""
 
-    def __new__(cls, ts):
+    def __new__(cls, ts, _trusted=None):
         q, s = ts
         self = super().__new__(cls, (q, s))
+        if _trusted is not None:
+            self.lead, self.rows, self.K, self.block_rows, self.dev = _trusted
+            return self
+        shape, s_shape = tuple(q.shape), tuple(s.shape)
         _need(q.dtype == _F8 and s.dtype == torch.float32, "q must be float8_e4m3fn and s fp32")
-        _need(2 <= q.dim() <= 3 and s.dim() == q.dim(), "q and s: 2-D, or 3-D with one per matrix")
-        shape, rows, K = tuple(q.shape), q.shape[-2], q.shape[-1]
-        _need(K % 16 == 0, f"q {shape}: K must be a multiple of 16")
-        head, n = (*shape[:-2], -(-K // 128)), s.shape[-1]
-        _need(tuple(s.shape[:-1]) == head and n in (rows, -(-rows // 128)),
-              f"q {shape} and s {tuple(s.shape)} do not belong together")
+        _need(2 <= len(shape) <= 3 and len(s_shape) == len(shape),
+              "q and s: 2-D, or 3-D with one per matrix")
+        rows, K = shape[-2:]
+        n = s_shape[-1]
+        if K % 16 != 0 or s_shape[:-1] != (*shape[:-2], -(-K // 128)) or n not in (rows, -(-rows // 128)):
+            raise ValueError(f"q {shape} and s {s_shape} do not belong together (K % 16 == 0, "
+                             "s [.., ceil(K/128), rows or ceil(rows/128)])")
         _need(q.is_contiguous() and s.is_contiguous(), "q and s must be contiguous")
         dev = q.get_device()
         _need(q.is_cuda and s.get_device() == dev, "q and s must be on one GPU")
@@ -604,33 +622,37 @@ def nvfp4_fp8_grouped_wgrad_raw(G, m_offsets, total_m, N, K, a_q, a_s, b_q, b_s,
                                           dw_dtype, flags, _stream(stream))
 
 
-def _fp8_buffers(layout: str, out, rows_shape, s_shape, cols_shape, st_shape, device, dev: int):
-    """The operands a quantiser writes, new or the caller's (checked):
-    {"rows": Fp8Packed, "cols": Fp8Packed} of the layouts asked for."""
-    _need(layout in ("rows", "cols", "both"), "layout: 'rows', 'cols' or 'both'")
-    names = ("rows", "cols") if layout == "both" else (layout,)
-    given = None if out is None else (tuple(out) if layout == "both" else (out,))
-    _need(given is None or len(given) == len(names), "out: one operand per layout")
-    res = {}
-    for i, n in enumerate(names):
-        q_shape, sc_shape = (rows_shape, s_shape) if n == "rows" else (cols_shape, st_shape)
-        if given is None:
-            res[n] = Fp8Packed((torch.empty(q_shape, dtype=_F8, device=device),
-                                torch.empty(sc_shape, dtype=torch.float32, device=device)))
-        else:
-            o = _fp8(given[i])
-            _need(tuple(o[0].shape) == q_shape and tuple(o[1].shape) == sc_shape and o.dev == dev,
-                  f"out: expected q {q_shape} and s {sc_shape} on x's GPU")
-            res[n] = o
-    return res
+def _fp8_buffer(out, q_shape, s_shape, block_rows: int, x, dev: int) -> Fp8Packed:
+    """The operand a quantiser writes: new, or the caller's (checked)."""
+    if out is None:
+        return Fp8Packed((x.new_empty(q_shape, dtype=_F8), x.new_empty(s_shape, dtype=torch.float32)),
+                         _trusted=(q_shape[:-2], q_shape[-2], q_shape[-1], block_rows, dev))
+    o = _fp8(out)
+    if tuple(o[0].shape) != q_shape or tuple(o[1].shape) != s_shape or o.dev != dev:
+        raise ValueError(f"out: expected q {q_shape} and s {s_shape} on x's GPU")
+    return o
 
 
-def _fp8_ptrs(res):
-    return [None if n not in res else _ptr(t) for n in ("rows", "cols") for t in res.get(n, (None, None))]
+def _fp8_buffers(layout: str, out, rows_shapes, cols_shapes, block_rows: int, x, dev: int):
+    """(rows operand or None, transposed operand or None) of a layout."""
+    if layout == "rows":
+        return _fp8_buffer(out, *rows_shapes, block_rows, x, dev), None
+    if layout == "cols":
+        return None, _fp8_buffer(out, *cols_shapes, block_rows, x, dev)
+    _need(layout == "both", "layout: 'rows', 'cols' or 'both'")
+    _need(out is None or len(out) == 2, "out: one operand per layout")
+    r, c = (None, None) if out is None else out
+    return (_fp8_buffer(r, *rows_shapes, block_rows, x, dev),
+            _fp8_buffer(c, *cols_shapes, block_rows, x, dev))
 
 
-def _fp8_result(layout: str, res):
-    return (res["rows"], res["cols"]) if layout == "both" else res[layout]
+def _fp8_ptrs(rows, cols):
+    return (None if rows is None else rows[0].data_ptr(), None if rows is None else rows[1].data_ptr(),
+            None if cols is None else cols[0].data_ptr(), None if cols is None else cols[1].data_ptr())
+
+
+def _fp8_result(rows, cols):
+    return cols if rows is None else rows if cols is None else (rows, cols)
 
 
 def nvfp4_fp8_quantize(x: torch.Tensor, block_rows: int = 1, layout: str = "rows", out=None,
@@ -641,25 +663,33 @@ def nvfp4_fp8_quantize(x: torch.Tensor, block_rows: int = 1, layout: str = "rows
     [.., cols, rows rounded up to 16]; "both": the two from one read, as a
     pair.  block_rows 1 scales 1 x 128 blocks, 128 scales 128 x 128 blocks
     (weights).  ``out`` reuses buffers."""
-    _need(x.dim() in (2, 3) and x.dtype in _DT_IN, "x: 2-D or 3-D, fp32 or bf16")
+    dt = _DT_IN.get(x.dtype)
+    _need(dt is not None and x.dim() in (2, 3), "x: 2-D or 3-D, fp32 or bf16")
     _need(x.is_cuda, "x: must be on a GPU")
     _need(block_rows in (1, 128), "block_rows: 1 or 128")
-    lead, (rows, cols) = tuple(x.shape[:-2]), x.shape[-2:]
+    _need(x.shape[-1] % 16 == 0, "x: columns must be a multiple of 16")
+    dev = x.get_device()
+    if _here(stream, dev):
+        return _fp8_quantize(x, dt, block_rows, layout, out, dev)
+    with _there(stream, dev):
+        return _fp8_quantize(x, dt, block_rows, layout, out, dev)
+
+
+def _fp8_quantize(x, dt: int, block_rows: int, layout: str, out, dev: int):
+    *lead, rows, cols = x.shape
     batch = lead[0] if lead else 1
-    _need(cols % 16 == 0, "x: columns must be a multiple of 16")
     ld = _stride(x, cols, "x")
     _need(batch <= 1 or x.stride(0) == rows * ld, "x: matrices must follow each other")
-    dev = x.get_device()
-    rows_t = -(-rows // 16) * 16
-    with _on_gpu(dev), _on_stream(stream, dev):
-        res = _fp8_buffers(layout, out, (*lead, rows, cols), (*lead, -(-cols // 128), -(-rows // block_rows)),
-                           (*lead, cols, rows_t),
-                           (*lead, -(-rows_t // 128), cols if block_rows == 1 else -(-cols // 128)),
-                           x.device, dev)
-        st = nvfp4_fp8_quantize_raw(_ptr(x), _DT_IN[x.dtype], batch, rows, cols, ld, block_rows,
-                                    *_fp8_ptrs(res), _stream(None, dev))
-    _check("nvfp4_fp8_quantize", st)
-    return _fp8_result(layout, res)
+    rows_t, kb = -(-rows // 16) * 16, -(-cols // 128)
+    r, c = _fp8_buffers(
+        layout, out, ((*lead, rows, cols), (*lead, kb, -(-rows // block_rows))),
+        ((*lead, cols, rows_t), (*lead, -(-rows_t // 128), cols if block_rows == 1 else kb)),
+        block_rows, x, dev)
+    st = nvfp4_fp8_quantize_raw(x.data_ptr(), dt, batch, rows, cols, ld, block_rows,
+                                *_fp8_ptrs(r, c), _stream(None, dev))
+    if st != NVFP4_OK:
+        _check("nvfp4_fp8_quantize", st)
+    return _fp8_result(r, c)
 
 
 def _groups(m_offsets, dev: int, G: int | None = None) -> int:
@@ -695,26 +725,27 @@ def nvfp4_fp8_grouped_quantize(x: torch.Tensor, m_offsets: torch.Tensor, layout:
     _row_index(row_index, total, dev)
     _need(G > 0 or total == 0, "m_offsets: no groups for the rows")
     P = nvfp4_fp8_grouped_columns(total, G)
-    with _on_gpu(dev), _on_stream(stream, dev):
-        res = _fp8_buffers(layout, out, (total, cols), (-(-cols // 128), total), (cols, P),
-                           (P // 128, cols), x.device, dev)
+    with contextlib.nullcontext() if _here(stream, dev) else _there(stream, dev):
+        r, c = _fp8_buffers(layout, out, ((total, cols), (-(-cols // 128), total)),
+                            ((cols, P), (P // 128, cols)), 1, x, dev)
         st = nvfp4_fp8_grouped_quantize_raw(_ptr(x), _DT_IN[x.dtype], G, _ptr(m_offsets),
                                             None if row_index is None else _ptr(row_index), total,
-                                            x_rows, cols, ld, *_fp8_ptrs(res), _stream(None, dev))
+                                            x_rows, cols, ld, *_fp8_ptrs(r, c), _stream(None, dev))
     _check("nvfp4_fp8_grouped_quantize", st)
-    return _fp8_result(layout, res)
+    return _fp8_result(r, c)
 
 
-def _fp8_out(y, shape, out_dtype: str, accumulate: bool, device, dev: int):
+def _fp8_out(y, shape, out_dtype: str, accumulate: bool, like, dev: int):
     """The output (new, or the caller's, checked), its dtype code and row stride."""
-    _need(out_dtype in _DT_OUT, f"out_dtype: one of {sorted(_DT_OUT)}")
-    code, tdt = _DT_OUT[out_dtype]
-    _need(not accumulate or (y is not None and out_dtype == "f32"),
-          "accumulate: needs an fp32 output to add to")
+    code_dt = _DT_OUT.get(out_dtype)
+    _need(code_dt is not None, "out_dtype: 'f32' or 'bf16'")
+    code, tdt = code_dt
     if y is None:
-        y = torch.empty(shape, dtype=tdt, device=device)
-    _need(y.dtype == tdt, f"y: dtype {y.dtype}, expected {tdt}")
-    _need(tuple(y.shape) == tuple(shape), f"y: shape {tuple(y.shape)}, expected {tuple(shape)}")
+        _need(not accumulate, "accumulate: needs an fp32 output to add to")
+        return like.new_empty(shape, dtype=tdt), code, shape[-1]
+    _need(not accumulate or code == NVFP4_F32, "accumulate: needs an fp32 output to add to")
+    if y.dtype != tdt or tuple(y.shape) != shape:
+        raise ValueError(f"y: {tuple(y.shape)} {y.dtype}, expected {shape} {tdt}")
     _on_dev(y, dev, "y")
     return y, code, _stride(y, shape[-1], "y")
 
@@ -730,13 +761,21 @@ def nvfp4_fp8_gemm(a, b, out_dtype: str = "bf16", y: torch.Tensor | None = None,
     _need(not a.lead and not b.lead and a.K == b.K and a.dev == b.dev,
           "a and b: 2-D operands with the same K on one GPU")
     _need(a.block_rows == 1, "a: must have block_rows 1")
-    M, N, K, dev = a.rows, b.rows, a.K, a.dev
-    with _on_gpu(dev), _on_stream(stream, dev):
-        y, code, ld = _fp8_out(y, (M, N), out_dtype, accumulate, a[0].device, dev)
-        st = nvfp4_fp8_gemm_raw(M, N, K, _ptr(a[0]), _ptr(a[1]), _ptr(b[0]), _ptr(b[1]), b.block_rows,
-                                _ptr(y), code, ld, NVFP4_ACCUMULATE if accumulate else 0,
-                                _stream(None, dev))
-    _check("nvfp4_fp8_gemm", st)
+    if _here(stream, a.dev):
+        return _fp8_gemm(a, b, out_dtype, y, accumulate)
+    with _there(stream, a.dev):
+        return _fp8_gemm(a, b, out_dtype, y, accumulate)
+
+
+def _fp8_gemm(a, b, out_dtype: str, y, accumulate: bool):
+    a_q, a_s = a
+    b_q, b_s = b
+    y, code, ld = _fp8_out(y, (a.rows, b.rows), out_dtype, accumulate, a_q, a.dev)
+    st = nvfp4_fp8_gemm_raw(a.rows, b.rows, a.K, a_q.data_ptr(), a_s.data_ptr(), b_q.data_ptr(),
+                            b_s.data_ptr(), b.block_rows, y.data_ptr(), code, ld,
+                            NVFP4_ACCUMULATE if accumulate else 0, _stream(None, a.dev))
+    if st != NVFP4_OK:
+        _check("nvfp4_fp8_gemm", st)
     return y
 
 
@@ -756,8 +795,8 @@ def nvfp4_fp8_grouped_gemm(m_offsets: torch.Tensor, total_m: int, a, b, out_dtyp
     dev = b.dev
     G = _groups(m_offsets, dev, b.lead[0])
     _row_index(row_index, total_m, dev)
-    with _on_gpu(dev), _on_stream(stream, dev):
-        y, code, ld = _fp8_out(y, (total_m, b.rows), out_dtype, False, b[0].device, dev)
+    with contextlib.nullcontext() if _here(stream, dev) else _there(stream, dev):
+        y, code, ld = _fp8_out(y, (total_m, b.rows), out_dtype, False, b[0], dev)
         st = nvfp4_fp8_grouped_gemm_raw(G, _ptr(m_offsets),
                                         None if row_index is None else _ptr(row_index), total_m,
                                         a.rows, b.rows, b.K, _ptr(a[0]), _ptr(a[1]), _ptr(b[0]),
@@ -777,11 +816,11 @@ def nvfp4_fp8_grouped_wgrad(m_offsets: torch.Tensor, total_m: int, a, b, out_dty
     _need(a.block_rows == 1 and b.block_rows == 1, "a and b: must have block_rows 1")
     dev = a.dev
     G = _groups(m_offsets, dev)
-    _need(a.K == nvfp4_fp8_grouped_columns(total_m, G),
-          f"a and b: {a.K} columns, expected nvfp4_fp8_grouped_columns({total_m}, {G})")
+    if a.K != nvfp4_fp8_grouped_columns(total_m, G):
+        raise ValueError(f"a and b: {a.K} columns, expected nvfp4_fp8_grouped_columns({total_m}, {G})")
     _need(G > 0 or total_m == 0, "m_offsets: no groups for the rows")
-    with _on_gpu(dev), _on_stream(stream, dev):
-        dw, code, ld = _fp8_out(dw, (G, a.rows, b.rows), out_dtype, accumulate, a[0].device, dev)
+    with contextlib.nullcontext() if _here(stream, dev) else _there(stream, dev):
+        dw, code, ld = _fp8_out(dw, (G, a.rows, b.rows), out_dtype, accumulate, a[0], dev)
         _need(dw.is_contiguous(), "dw: must be contiguous")
         st = nvfp4_fp8_grouped_wgrad_raw(G, _ptr(m_offsets), total_m, a.rows, b.rows, _ptr(a[0]),
                                          _ptr(a[1]), _ptr(b[0]), _ptr(b[1]), _ptr(dw), code,
@@ -848,28 +887,38 @@ def nvfp4_moe_route(logits: torch.Tensor, topk: int, mask: torch.Tensor | None =
     and the balance loss.  ``mask`` [T]: tokens at 0 are not routed.
     ``renormalize``: weights are the softmax over the chosen experts."""
     T, E, ld, dev = _logits(logits, mask)
-    n = T * topk
-    _need(1 <= topk <= E, f"topk: 1 to {E}")
-    need = nvfp4_moe_route_workspace_bytes(T, E)
+    _need(1 <= topk <= E, "topk: 1 to the number of experts")
     if workspace is not None:
         _on_dev(workspace, dev, "workspace")
         _need(workspace.is_contiguous(), "workspace: must be contiguous")
-    with _on_gpu(dev), _on_stream(stream, dev):
-        # one allocation for the outputs; a tail of it is the workspace
-        own = 0 if workspace is not None else -(-need // 4)
-        buf = torch.empty(4 * n + 2 * E + 3 + own, dtype=torch.int32, device=logits.device)
-        ei, w, ri, pr, counts, off, routed, loss, ws = buf.split_with_sizes((n, n, n, n, E, E + 1, 1, 1, own))
-        r = MoeRoute(ei.view(T, topk), w.view(torch.float32).view(T, topk), counts, off, ri,
-                     pr.view(T, topk), routed, loss.view(torch.float32))
-        ws = ws if workspace is None else workspace
-        st = nvfp4_moe_route_raw(T, E, topk, _ptr(logits), _DT_IN[logits.dtype], ld,
-                                 None if mask is None else _ptr(mask),
-                                 NVFP4_ROUTE_RENORMALIZE if renormalize else 0,
-                                 _ptr(r.expert_index), _ptr(r.weights), _ptr(counts), _ptr(off),
-                                 _ptr(ri), _ptr(r.pair_row), _ptr(routed), _ptr(r.loss), _ptr(ws),
-                                 ws.numel() * ws.element_size(), _stream(None, dev))
-    _check("nvfp4_moe_route", st)
-    return r
+    if _here(stream, dev):
+        return _moe_route(logits, topk, mask, renormalize, workspace, T, E, ld, dev)
+    with _there(stream, dev):
+        return _moe_route(logits, topk, mask, renormalize, workspace, T, E, ld, dev)
+
+
+def _moe_route(logits, topk: int, mask, renormalize: bool, workspace, T: int, E: int, ld: int,
+               dev: int) -> MoeRoute:
+    n = T * topk
+    need = nvfp4_moe_route_workspace_bytes(T, E) if workspace is None else 0
+    # one allocation for the outputs; its tail is the workspace
+    buf = logits.new_empty(4 * n + 2 * E + 3 + -(-need // 4), dtype=torch.int32)
+    ei, w, ri, pr, counts, off, routed, loss, _ = buf.split_with_sizes(
+        (n, n, n, n, E, E + 1, 1, 1, -(-need // 4)))
+    p = buf.data_ptr()
+    at = p + 16 * n               # counts, m_offsets, routed, loss, workspace
+    ws, ws_bytes = at + 8 * E + 12, need
+    if workspace is not None:
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    st = nvfp4_moe_route_raw(T, E, topk, logits.data_ptr(), _DT_IN[logits.dtype], ld,
+                             None if mask is None else mask.data_ptr(),
+                             NVFP4_ROUTE_RENORMALIZE if renormalize else 0, p, p + 4 * n, at,
+                             at + 4 * E, p + 8 * n, p + 12 * n, at + 8 * E + 4, at + 8 * E + 8, ws,
+                             ws_bytes, _stream(None, dev))
+    if st != NVFP4_OK:
+        _check("nvfp4_moe_route", st)
+    return MoeRoute(ei.view(T, topk), w.view(torch.float32).view(T, topk), counts, off, ri,
+                    pr.view(T, topk), routed, loss.view(torch.float32))
 
 
 def nvfp4_moe_route_backward(logits: torch.Tensor, route: MoeRoute,
@@ -895,9 +944,9 @@ def nvfp4_moe_route_backward(logits: torch.Tensor, route: MoeRoute,
     if d_loss is not None:
         _need(d_loss.dtype == torch.float32 and d_loss.numel() == 1, "d_loss: one fp32 value")
         _on_dev(d_loss, dev, "d_loss")
-    with _on_gpu(dev), _on_stream(stream, dev):
+    with contextlib.nullcontext() if _here(stream, dev) else _there(stream, dev):
         if out is None:
-            out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+            out = logits.new_empty((T, E))
         _need(out.dtype == logits.dtype and tuple(out.shape) == (T, E), "out: the logits' dtype and shape")
         _on_dev(out, dev, "out")
         st = nvfp4_moe_route_backward_raw(T, E, topk, _ptr(logits), _DT_IN[logits.dtype], ld,
