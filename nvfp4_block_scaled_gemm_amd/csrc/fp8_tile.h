@@ -126,6 +126,11 @@ struct Tile {
     const int wm = wave / WN, wn = wave % WN;
     const int li = lane & 15, lg = lane >> 4;
     const int nk = (int)((K + kBlock - 1) / kBlock);
+    // plain copies: a choice between two fields stays a choice of registers
+    const uint8_t *const aq = A.q, *const bq = B.q;
+    const float *const as = A.s, *const bs = B.s;
+    const int64_t as_ld = A.s_ld, bs_ld = B.s_ld;
+    const uint32_t aq_bytes = A.q_bytes, bq_bytes = B.q_bytes, as_bytes = A.s_bytes, bs_bytes = B.s_bytes;
 
     uint32_t a_off[kALoads], b_off[kBLoads], s_off[kSLoads];
     // a load's 16-byte chunk of its rows; rows 8 apart only flip fixed bits
@@ -193,17 +198,17 @@ struct Tile {
       const uint32_t soff = (uint32_t)s * kBlock;
       if constexpr (J < kBLoads) {
         constexpr int i = J;
-        load_lds16(make_rsrc(B.q, live ? B.q_bytes : 0u), base + kBOff + (wave * kBLoads + i) * 1024,
+        load_lds16(make_rsrc(bq, live ? bq_bytes : 0u), base + kBOff + (wave * kBLoads + i) * 1024,
                    cut && b_past[i] ? kNoRow : b_off[i], soff);
       } else if constexpr (J < kBLoads + kALoads) {
         constexpr int i = J - kBLoads;
-        load_lds16(make_rsrc(A.q, live ? A.q_bytes : 0u), base + kAOff + (wave * kALoads + i) * 1024,
+        load_lds16(make_rsrc(aq, live ? aq_bytes : 0u), base + kAOff + (wave * kALoads + i) * 1024,
                    cut && a_past[i] ? kNoRow : a_off[i], soff);
       } else {
         constexpr int i = J - kBLoads - kALoads;
-        const float* p = s_is_a[i] ? A.s : B.s;
-        const int64_t at = (int64_t)max(min(s, nk - 1), 0) * (s_is_a[i] ? A.s_ld : B.s_ld);
-        const uint32_t bytes = s_is_a[i] ? A.s_bytes : B.s_bytes;
+        const float* p = s_is_a[i] ? as : bs;
+        const int64_t at = (int64_t)max(min(s, nk - 1), 0) * (s_is_a[i] ? as_ld : bs_ld);
+        const uint32_t bytes = s_is_a[i] ? as_bytes : bs_bytes;
         load_lds4(make_rsrc(p + at, live ? bytes : 0u), base + kSOff + s_slot[i] * 256, s_off[i], 0);
       }
     };
@@ -259,6 +264,23 @@ struct Tile {
     issue(STAGES - 1, STAGES - 1, std::integral_constant<int, EARLY>{});
     wait_vmcnt<(STAGES - 2) * kLoads + EARLY>();
     workgroup_barrier();
+    if (wm * TM >= out.m || wn * TN >= out.n) {
+      // no output of this wave exists (a group's last rows): it only loads
+      // and meets the others, and leaves the matrix core to the wave beside it
+      int slot = 0;
+      for (int s = 0; s < nk; ++s) {
+        static_for<kLoads - EARLY>([&](auto nc) {
+          load_one(s + STAGES - 1, slot == 0 ? STAGES - 1 : slot - 1, std::integral_constant<int, EARLY + decltype(nc)::value>{});
+        });
+        wait_vmcnt<(STAGES - 2) * kLoads>();
+        workgroup_barrier();
+        issue(s + STAGES, slot, std::integral_constant<int, EARLY>{});
+        slot = slot + 1 == STAGES ? 0 : slot + 1;
+      }
+      wait_vmcnt<0>();
+      workgroup_barrier();  // the others' turn to the ring for their outputs
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < FN; ++i) br[i] = read_b(smem, i);
 #pragma unroll
