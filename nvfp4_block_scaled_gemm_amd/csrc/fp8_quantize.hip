@@ -15,7 +15,7 @@
 //    one read, one write, no shared memory;
 //  * anything that needs a column's or a 128 x 128 block's maximum, or the
 //    transposed bytes: a workgroup holds one 128 x 128 tile in registers,
-//    each thread 8 rows x 8 columns, so x is read once for all outputs.
+//    each thread 4 rows x 8 columns, so x is read once for all outputs.
 //    Row maxima join 16 lanes, column maxima the workgroup through LDS, and
 //    the transposed bytes leave through a 16 KB LDS tile in whole 128-byte
 //    rows.
@@ -43,10 +43,10 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits) {
   return {finite ? a / kTop : __uint_as_float(0x7FC00000u), kTop / a, finite};
 }
 
-__device__ __forceinline__ u32x2 encode8(const float* v, const BlockScale& b) {
-  u32x2 w = {encode4(v[0] * b.r, v[1] * b.r, v[2] * b.r, v[3] * b.r),
-             encode4(v[4] * b.r, v[5] * b.r, v[6] * b.r, v[7] * b.r)};
-  if (!b.finite) w = u32x2{0, 0};
+__device__ __forceinline__ u32x2 encode8(const float* v, float r, bool finite) {
+  u32x2 w = {encode4(v[0] * r, v[1] * r, v[2] * r, v[3] * r),
+             encode4(v[4] * r, v[5] * r, v[6] * r, v[7] * r)};
+  if (!finite) w = u32x2{0, 0};
   return w;
 }
 
@@ -77,11 +77,17 @@ __device__ __forceinline__ uint32_t amax8(const float* v) {
   return m;
 }
 
-// Largest over the 16 lanes of a row group (all lanes receive it).
+// Largest over the 16 lanes of a row group (all lanes receive it): rotations
+// inside the group, no LDS.
+template <int N>
+__device__ __forceinline__ uint32_t ror16(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + N, 0xF, 0xF, false);
+}
 __device__ __forceinline__ uint32_t max16(uint32_t m) {
-#pragma unroll
-  for (int d = 1; d < 16; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d, 64));
-  return m;
+  m = max(m, ror16<8>(m));
+  m = max(m, ror16<4>(m));
+  m = max(m, ror16<2>(m));
+  return max(m, ror16<1>(m));
 }
 
 // Rows layout, 1 x 128 blocks: workgroup (block of K, run of 16 * ROWS rows).
@@ -110,7 +116,7 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const void* __restri
     const int64_t r = r0 + 16 * i;
     const BlockScale b = block_scale(max16(amax8(v[i])));
     if (r < rows) {
-      if (col < cols) *reinterpret_cast<u32x2*>(q + r * cols + col) = encode8(v[i], b);
+      if (col < cols) *reinterpret_cast<u32x2*>(q + r * cols + col) = encode8(v[i], b.r, b.finite);
       if ((threadIdx.x & 15) == 0) s[(int64_t)kb * rows + r] = b.s;
     }
   }
@@ -124,24 +130,37 @@ struct QuantTile {
   int64_t dst_col;   // first column in the transposed layout
 };
 
-// One 128 x 128 tile.  BLK: one scale for the tile; else 1 x 128 blocks along
-// each layout's own axis.
+// One 128 x 128 tile by 512 threads, 4 rows x 8 columns each (8 x 8 by 256
+// threads: 155 registers, three waves a SIMD and 152 instead of 127 us for
+// 32768 x 4096 bf16 in both layouts).  BLK: one scale for the tile; else 1 x
+// 128 blocks along each layout's own axis.
+constexpr int kTileThreads = 512, kTileRows = 4, kTileWaves = kTileThreads / 64;
+
+// Byte of row r (a multiple of 4) of column c in the transposed tile: chunks
+// of 16 rows move with the column's group of 8, which is the lane, so that a
+// wave's writes spread over the banks.
+__device__ __forceinline__ int turned_at(int c, int r) {
+  return c * kBlock + ((((r >> 4) ^ ((c >> 3) & 7)) << 4) | (r & 15));
+}
+
 template <int DT, bool BLK>
 __device__ __forceinline__ void quantize_tile(
     const void* __restrict__ x, int64_t ld_x, int64_t cols, const int32_t* __restrict__ index,
     int64_t x_rows, const QuantTile& t, int64_t kb, uint8_t* __restrict__ q, float* __restrict__ s,
     int64_t s_ld, int64_t s_row, uint8_t* __restrict__ qt, int64_t ld_t, int64_t t_limit,
     float* __restrict__ st, int64_t st_ld, int64_t st_row) {
-  __shared__ uint32_t part[4][kBlock];
+  constexpr int R = kTileRows;
+  __shared__ uint32_t part[kTileWaves][kBlock], rowpart[kBlock];
+  __shared__ __attribute__((aligned(16))) float mul[2][kBlock];  // reciprocals: rows, columns
   __shared__ __attribute__((aligned(16))) uint8_t turned[kBlock * kBlock];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int rg = tid >> 4, cg = tid & 15;  // 8 rows from 8 * rg, 8 columns from 8 * cg
+  const int r0 = (tid >> 4) * R, cg = tid & 15;  // rows from r0, columns from 8 * cg
   const int64_t col = kb * kBlock + cg * 8;
   const bool col_in = col < cols;
-  float v[8][8];
+  float v[R][8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = rg * 8 + i;
+  for (int i = 0; i < R; ++i) {
+    const int r = r0 + i;
     int64_t src = t.src_row + r;
     bool in = r < t.rows && col_in;
     if (index != nullptr && r < t.rows) {
@@ -155,95 +174,113 @@ __device__ __forceinline__ void quantize_tile(
       for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
     }
   }
-  uint32_t colmax[8], rowmax[8];
+  // maxima: a block's scale is computed by one thread and read by those that
+  // encode (two divisions a block, not a lane)
+  uint32_t colmax[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) colmax[j] = 0;
+  for (int j = 0; j < 8; ++j) {
+    colmax[j] = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    rowmax[i] = amax8(v[i]);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) colmax[j] = max(colmax[j], __float_as_uint(v[i][j]) & 0x7FFFFFFFu);
+    for (int i = 0; i < R; ++i) colmax[j] = max(colmax[j], __float_as_uint(v[i][j]) & 0x7FFFFFFFu);
   }
   if constexpr (BLK) {
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, rowmax[i]);
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d, 64));
+    for (int j = 0; j < 8; ++j) m = max(m, colmax[j]);
+    m = max16(m);
+    m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
+    m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
     if (lane == 0) part[wave][0] = m;
     __syncthreads();
-    m = max(max(part[0][0], part[1][0]), max(part[2][0], part[3][0]));
+    m = 0;
+#pragma unroll
+    for (int w = 0; w < kTileWaves; ++w) m = max(m, part[w][0]);
     const BlockScale b = block_scale(m);
     if (tid == 0) {
       if (q != nullptr) s[kb * s_ld + s_row] = b.s;
       if (qt != nullptr) st[st_row * st_ld + kb] = b.s;
     }
-    u32x2 w[8];
+    u32x2 w[R];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      w[i] = encode8(v[i], b);
-      if (q != nullptr && rg * 8 + i < t.rows && col_in)
-        *reinterpret_cast<u32x2*>(q + (t.dst_row + rg * 8 + i) * cols + col) = w[i];
+    for (int i = 0; i < R; ++i) {
+      w[i] = encode8(v[i], b.r, b.finite);
+      if (q != nullptr && r0 + i < t.rows && col_in)
+        *reinterpret_cast<u32x2*>(q + (t.dst_row + r0 + i) * cols + col) = w[i];
     }
     if (qt == nullptr) return;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      u32x2 o = {0, 0};
+      uint32_t o = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i >> 2] |= ((w[i][j >> 2] >> (8 * (j & 3))) & 0xFFu) << (8 * (i & 3));
-      const int c = cg * 8 + j;
-      *reinterpret_cast<u32x2*>(turned + c * kBlock + ((rg ^ (cg & 15)) << 3)) = o;
+      for (int i = 0; i < R; ++i) o |= ((w[i][j >> 2] >> (8 * (j & 3))) & 0xFFu) << (8 * i);
+      *reinterpret_cast<uint32_t*>(turned + turned_at(cg * 8 + j, r0)) = o;
     }
   } else {
     if (q != nullptr) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const BlockScale b = block_scale(max16(rowmax[i]));
-        const int r = rg * 8 + i;
-        if (r < t.rows) {
-          if (col_in) *reinterpret_cast<u32x2*>(q + (t.dst_row + r) * cols + col) = encode8(v[i], b);
-          if (cg == 0) s[kb * s_ld + s_row + r] = b.s;
-        }
+      for (int i = 0; i < R; ++i) {
+        const uint32_t m = max16(amax8(v[i]));
+        if (cg == 0) rowpart[r0 + i] = m;
+      }
+    }
+    if (qt != nullptr) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        uint32_t m = colmax[j];
+        m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
+        m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
+        if (lane < 16) part[wave][cg * 8 + j] = m;
+      }
+    }
+    __syncthreads();
+    const int at = tid & (kBlock - 1);
+    if (tid < kBlock) {
+      if (q != nullptr) {
+        const BlockScale b = block_scale(rowpart[at]);
+        mul[0][at] = b.finite ? b.r : -1.f;
+        if (at < t.rows) s[kb * s_ld + s_row + at] = b.s;
+      }
+    } else if (tid < 2 * kBlock && qt != nullptr) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int w = 0; w < kTileWaves; ++w) m = max(m, part[w][at]);
+      const BlockScale b = block_scale(m);
+      mul[1][at] = b.finite ? b.r : -1.f;
+      if (kb * kBlock + at < cols) st[st_row * st_ld + kb * kBlock + at] = b.s;
+    }
+    __syncthreads();
+    if (q != nullptr) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const float m = mul[0][r0 + i];
+        if (r0 + i < t.rows && col_in)
+          *reinterpret_cast<u32x2*>(q + (t.dst_row + r0 + i) * cols + col) = encode8(v[i], m, m >= 0.f);
       }
     }
     if (qt == nullptr) return;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      uint32_t m = colmax[j];
-      m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
-      m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
-      if (lane < 16) part[wave][cg * 8 + j] = m;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int c = cg * 8 + j;
-      const BlockScale b = block_scale(max(max(part[0][c], part[1][c]), max(part[2][c], part[3][c])));
-      if (rg == 0 && col + j < cols) st[st_row * st_ld + kb * kBlock + c] = b.s;
-      float u[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) u[i] = v[i][j];
-      *reinterpret_cast<u32x2*>(turned + c * kBlock + ((rg ^ (cg & 15)) << 3)) = encode8(u, b);
+      const float m = mul[1][cg * 8 + j];
+      const uint32_t o = encode4(v[0][j] * m, v[1][j] * m, v[2][j] * m, v[3][j] * m);
+      *reinterpret_cast<uint32_t*>(turned + turned_at(cg * 8 + j, r0)) = m >= 0.f ? o : 0u;
     }
   }
   __syncthreads();
-  // transposed rows: 16 bytes per thread, 8 threads a row, 32 rows a pass
+  // transposed rows: 16 bytes per thread, 8 threads a row
 #pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    const int c = p * 32 + (tid >> 3), k = (tid & 7) * 2, sw = (c >> 3) & 15;
-    const int64_t at = t.dst_col + k * 8;
-    if (kb * kBlock + c < cols && at < t_limit) {
-      const u32x2 lo = *reinterpret_cast<const u32x2*>(turned + c * kBlock + ((k ^ sw) << 3));
-      const u32x2 hi = *reinterpret_cast<const u32x2*>(turned + c * kBlock + (((k + 1) ^ sw) << 3));
-      *reinterpret_cast<u32x4*>(qt + (kb * kBlock + c) * ld_t + at) = u32x4{lo[0], lo[1], hi[0], hi[1]};
-    }
+  for (int p = 0; p < kBlock * 8 / kTileThreads; ++p) {
+    const int c = p * (kTileThreads / 8) + (tid >> 3), r = (tid & 7) * 16;
+    const int64_t at = t.dst_col + r;
+    if (kb * kBlock + c < cols && at < t_limit)
+      *reinterpret_cast<u32x4*>(qt + (kb * kBlock + c) * ld_t + at) =
+          *reinterpret_cast<const u32x4*>(turned + turned_at(c, r));
   }
 }
 
 // Matrices of one batch, 128 x 128 tiles; transposed rows are `rows` rounded
 // up to 16 bytes (t_limit).
 template <int DT, bool BLK>
-__global__ __launch_bounds__(256) void quantize_tile_kernel(
+__global__ __launch_bounds__(kTileThreads) void quantize_tile_kernel(
     const void* __restrict__ x, int64_t rows, int64_t cols, int64_t ld_x, int kblocks, int rblocks,
     uint8_t* __restrict__ q, float* __restrict__ s, uint8_t* __restrict__ qt,
     float* __restrict__ st) {
@@ -264,7 +301,7 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(
 // whose running block count passes it; blocks behind the last expert are
 // zero blocks.
 template <int DT>
-__global__ __launch_bounds__(256) void quantize_grouped_kernel(
+__global__ __launch_bounds__(kTileThreads) void quantize_grouped_kernel(
     const void* __restrict__ x, int G, const int32_t* __restrict__ offsets,
     const int32_t* __restrict__ index, int64_t total_m, int64_t x_rows, int64_t cols, int64_t ld_x,
     int64_t P, int kblocks, uint8_t* __restrict__ q, float* __restrict__ s,
@@ -311,7 +348,7 @@ hipError_t launch_fp8_quantize(const void* x, int dtype, int64_t batch, int64_t 
   auto kern = block_rows == 1
                   ? (dtype == 1 ? quantize_tile_kernel<1, false> : quantize_tile_kernel<0, false>)
                   : (dtype == 1 ? quantize_tile_kernel<1, true> : quantize_tile_kernel<0, true>);
-  kern<<<(unsigned)grid, 256, 0, stream>>>(x, rows, cols, ld_x, (int)kblocks, (int)rblocks, q, s, qt, st);
+  kern<<<(unsigned)grid, kTileThreads, 0, stream>>>(x, rows, cols, ld_x, (int)kblocks, (int)rblocks, q, s, qt, st);
   return hipGetLastError();
 }
 
@@ -325,7 +362,7 @@ hipError_t launch_fp8_grouped_quantize(const void* x, int dtype, int32_t G,
   const int64_t grid = kblocks * (P / kBlock);
   if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
   auto kern = dtype == 1 ? quantize_grouped_kernel<1> : quantize_grouped_kernel<0>;
-  kern<<<(unsigned)grid, 256, 0, stream>>>(x, G, m_offsets, row_index, total_m, x_rows, cols, ld_x, P,
+  kern<<<(unsigned)grid, kTileThreads, 0, stream>>>(x, G, m_offsets, row_index, total_m, x_rows, cols, ld_x, P,
                                            (int)kblocks, q, s, qt, st);
   return hipGetLastError();
 }
