@@ -372,9 +372,10 @@ struct Tile {
     float* stage = reinterpret_cast<float*>(smem) + wave * 32 * RS;
     constexpr int LPR = TN / 8, RPI = 64 / LPR;  // lanes per row, rows per read
     constexpr int NP = 32 / RPI;
-    // whole rows of fp32: two runs of 16 bytes per lane, TN / 2 columns apart.
-    // What they add to is read ahead of everything, in one go.
-    const bool runs = WIDE && out.vec && (wn + 1) * TN <= out.n;
+    // Whole aligned rows leave in 16-byte pieces, fp32 ones as two runs TN / 2
+    // columns apart (what they add to is read ahead of everything, in one
+    // go); other rows element by element, a lane a column.
+    const bool runs = out.vec && (wn + 1) * TN <= out.n;
     float* const y32 = reinterpret_cast<float*>(out.y) + wn * TN + 4 * (lane % LPR);
     f32x4 old[WIDE ? FM / 2 : 1][WIDE ? NP : 1][2];
     if constexpr (WIDE) {
@@ -402,13 +403,12 @@ struct Tile {
 #pragma unroll
         for (int i = 0; i < FN; ++i)
           *reinterpret_cast<f32x4*>(stage + (16 * h + li) * RS + 32 * (i >> 1) + 8 * lg + 4 * (i & 1)) = acc[i][2 * j2 + h];
+      if (runs) {
 #pragma unroll
-      for (int p = 0; p < NP; ++p) {
-        const int r = p * RPI + lane / LPR;
-        const int m = wm * TM + 32 * j2 + r, c = lane % LPR;
-        bool done = false;
-        if constexpr (WIDE) {
-          if (runs) {
+        for (int p = 0; p < NP; ++p) {
+          const int r = p * RPI + lane / LPR, c = lane % LPR;
+          const int m = wm * TM + 32 * j2 + r;
+          if constexpr (WIDE) {
             const f32x4 lo = *reinterpret_cast<const f32x4*>(stage + r * RS + 4 * c);
             const f32x4 hi = *reinterpret_cast<const f32x4*>(stage + r * RS + TN / 2 + 4 * c);
             if (m < out.m) {
@@ -416,15 +416,27 @@ struct Tile {
               *reinterpret_cast<f32x4*>(y) = lo + old[j2][p][0];
               *reinterpret_cast<f32x4*>(y + TN / 2) = hi + old[j2][p][1];
             }
-            done = true;
+          } else {
+            const f32x4 lo = *reinterpret_cast<const f32x4*>(stage + r * RS + 8 * c);
+            const f32x4 hi = *reinterpret_cast<const f32x4*>(stage + r * RS + 8 * c + 4);
+            const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            if (m < out.m) store8(out, m, wn * TN + 8 * c, v);
           }
         }
-        if (!done) {
-          const int n = wn * TN + 8 * c;
-          const f32x4 lo = *reinterpret_cast<const f32x4*>(stage + r * RS + 8 * c);
-          const f32x4 hi = *reinterpret_cast<const f32x4*>(stage + r * RS + 8 * c + 4);
-          const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-          if (m < out.m && n < out.n) store8(out, m, n, v);
+      } else {
+#pragma unroll 4
+        for (int e = lane; e < 32 * TN; e += 64) {
+          const int r = e / TN, c = e % TN;
+          const int m = wm * TM + 32 * j2 + r, n = wn * TN + c;
+          if (m >= out.m || n >= out.n) continue;
+          const int64_t at = (int64_t)m * out.ld + n;
+          const float v = stage[r * RS + c];
+          if constexpr (WIDE) {
+            float* y = reinterpret_cast<float*>(out.y) + at;
+            *y = out.add ? *y + v : v;
+          } else {
+            reinterpret_cast<__bf16*>(out.y)[at] = (__bf16)v;
+          }
         }
       }
     }
