@@ -35,8 +35,8 @@ __device__ __forceinline__ TileOut out_of(const Fp8Out& y, int64_t at, int m, in
   return {(uint8_t*)y.y + at * es, y.ld, m, n, y.dtype, y.add, y.vec};
 }
 
-template <int BM, int BN, int WM, int WN, int STAGES, bool BROWS, bool WIDE>
-__global__ __launch_bounds__(64 * WM * WN, 2) void fp8_dense_kernel(int64_t M, int64_t N, int64_t K,
+template <int BM, int BN, int WM, int WN, int STAGES, int KG, bool BROWS, bool WIDE>
+__global__ __launch_bounds__(64 * WM * WN * KG, 2) void fp8_dense_kernel(int64_t M, int64_t N, int64_t K,
                                                                  Fp8Operand a, Fp8Operand b,
                                                                  Fp8Out y) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -47,7 +47,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_dense_kernel(int64_t M, i
   const int in = pid - group * 8 * tiles_n;
   const int64_t m0 = (int64_t)(first + in % gsz) * BM, n0 = (int64_t)(in / gsz) * BN;
   const int rm = (int)min((int64_t)BM, M - m0), rn = (int)min((int64_t)BN, N - n0);
-  using T = Tile<BM, BN, WM, WN, STAGES, BROWS, WIDE>;
+  using T = Tile<BM, BN, WM, WN, STAGES, KG, BROWS, WIDE>;
   T::template run<false>(rows_of(a.q, a.s, M, 1, m0, rm, K),
                          rows_of(b.q, b.s, BROWS ? N : ceil_div(N, kBlock), BROWS ? 1 : kBlock, n0, rn, K),
                          (uint32_t)K, (uint32_t)K, out_of(y, m0 * y.ld + n0, rm, rn), smem);
@@ -62,7 +62,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_grouped_kernel(
     int G, const int32_t* __restrict__ offsets, const int32_t* __restrict__ row_index,
     int64_t total_m, int64_t a_rows, int64_t N, int64_t K, Fp8Operand a, Fp8Operand b, Fp8Out y) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  using T = Tile<BM, BN, WM, WN, STAGES, false, WIDE>;
+  using T = Tile<BM, BN, WM, WN, STAGES, 1, false, WIDE>;
   const int lane = threadIdx.x & 63;
   const int64_t tiles_n = ceil_div(N, BN), nb = ceil_div(N, kBlock), kb = ceil_div(K, kBlock);
   const int step = gridDim.x;
@@ -112,7 +112,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_wgrad_kernel(
     int G, const int32_t* __restrict__ offsets, int64_t total_m, int64_t P, int64_t N, int64_t K,
     Fp8Operand a, Fp8Operand b, Fp8Out y) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  using T = Tile<BM, BN, WM, WN, STAGES, true, WIDE>;
+  using T = Tile<BM, BN, WM, WN, STAGES, 1, true, WIDE>;
   const int tiles_m = (int)ceil_div(N, BM), tiles_n = (int)ceil_div(K, BN);
   // every XCD takes an eighth of each expert's tiles, so that experts of
   // uneven load keep them all busy
@@ -149,22 +149,22 @@ hipError_t allow_lds(Kern kern, int bytes, std::atomic<uint64_t>& done) {
 }
 
 // A tile shape: BM x BN outputs by WM x WN waves with a ring of S stages.
-template <int BM_, int BN_, int WM_, int WN_, int S_>
+template <int BM_, int BN_, int WM_, int WN_, int S_, int KG_ = 1>
 struct Shape {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_, KG = KG_;
 };
 using S256x256 = Shape<256, 256, 2, 4, 2>;
 using S128x256 = Shape<128, 256, 2, 4, 3>;
 using S128x128 = Shape<128, 128, 2, 2, 2>;
-using S128x64 = Shape<128, 64, 2, 2, 3>;
+using S128x64 = Shape<128, 64, 2, 2, 3, 2>;
 using S64x128 = Shape<64, 128, 2, 2, 3>;
-using S64x64 = Shape<64, 64, 2, 2, 4>;
+using S64x64 = Shape<64, 64, 2, 2, 3, 2>;
 
 template <typename S, bool BROWS, bool WIDE>
 hipError_t dense(int64_t M, int64_t N, int64_t K, Fp8Operand a, Fp8Operand b, Fp8Out y,
                  hipStream_t stream) {
-  using T = Tile<S::BM, S::BN, S::WM, S::WN, S::S, BROWS, WIDE>;
-  auto kern = fp8_dense_kernel<S::BM, S::BN, S::WM, S::WN, S::S, BROWS, WIDE>;
+  using T = Tile<S::BM, S::BN, S::WM, S::WN, S::S, S::KG, BROWS, WIDE>;
+  auto kern = fp8_dense_kernel<S::BM, S::BN, S::WM, S::WN, S::S, S::KG, BROWS, WIDE>;
   static std::atomic<uint64_t> done{0};
   const hipError_t err = allow_lds(kern, T::kSmem, done);
   if (err != hipSuccess) return err;
@@ -185,24 +185,26 @@ int64_t shape_cost(int64_t M, int64_t N, int64_t bm, int64_t bn, int64_t t1, int
 
 // The shape with the least expected time.  Measured (us per block of 128,
 // one / two tiles on each CU): 8-bit products 256 x 256 1.70 / 3.40, 128 x 256
-// 1.18 / 2.36, 128 x 128 0.90 / 1.22, 128 x 64 0.49 / 0.75, 64 x 64
-// 0.36 / 0.55; wide ones 128 x 128 1.26 / 2.06, 128 x 64 0.79 / 1.27, 64 x 64
-// 0.60 / 0.80 (their larger shapes spill).  So 4096 x 8192 takes 256 x 256
+// 1.18 / 2.36, 128 x 128 0.90 / 1.22, 128 x 64 0.46 / 0.91, 64 x 64
+// 0.35 / 0.70; wide ones 128 x 128 1.26 / 2.06, 128 x 64 0.67 / 1.34, 64 x 64
+// 0.55 / 1.10 (their larger shapes spill).  So 4096 x 8192 takes 256 x 256
 // (230 us at K = 8192; 128 x 256: 290), 1024 x 8192 takes 128 x 256 (75;
-// 256 x 256: 99), 512 x 4096 takes 128 x 64 (24.4 at K = 6144; 128 x 128:
-// 41.8), 96 x 8192 takes 64 x 64 (23.3; 128 x 64: 30.7).
+// 256 x 256: 99), 512 x 4096 takes 128 x 64 (24.3 at K = 6144; 128 x 128:
+// 41.5), 96 x 8192 takes 64 x 64 (22.5 at K = 8192; 128 x 64: 29.2).  The two
+// smallest split K over two groups of waves (one group: 64 x 4096, K = 6144
+// 15.5 instead of 13.5 us; 203 x 8192, K = 8192 31.8 instead of 29.6).
 template <bool BROWS, bool WIDE>
 hipError_t dense_any(int64_t M, int64_t N, int64_t K, Fp8Operand a, Fp8Operand b, Fp8Out y,
                      hipStream_t stream) {
   constexpr int kShapes = WIDE ? 3 : 5;
   int64_t cost[kShapes];
   if constexpr (WIDE) {
-    cost[0] = shape_cost(M, N, 64, 64, 60, 80);
-    cost[1] = shape_cost(M, N, 128, 64, 79, 127);
+    cost[0] = shape_cost(M, N, 64, 64, 55, 110);
+    cost[1] = shape_cost(M, N, 128, 64, 67, 134);
     cost[2] = shape_cost(M, N, 128, 128, 126, 206);
   } else {
-    cost[0] = shape_cost(M, N, 64, 64, 36, 55);
-    cost[1] = shape_cost(M, N, 128, 64, 49, 75);
+    cost[0] = shape_cost(M, N, 64, 64, 35, 70);
+    cost[1] = shape_cost(M, N, 128, 64, 46, 91);
     cost[2] = shape_cost(M, N, 128, 128, 90, 122);
     cost[3] = shape_cost(M, N, 128, 256, 118, 236);
     cost[4] = shape_cost(M, N, 256, 256, 170, 340);
@@ -223,7 +225,7 @@ template <typename S, bool GATHER, bool WIDE>
 hipError_t grouped(int32_t G, const int32_t* m_offsets, const int32_t* row_index, int64_t total_m,
                    int64_t a_rows, int64_t N, int64_t K, Fp8Operand a, Fp8Operand b, Fp8Out y,
                    hipStream_t stream) {
-  using T = Tile<S::BM, S::BN, S::WM, S::WN, S::S, false, WIDE>;
+  using T = Tile<S::BM, S::BN, S::WM, S::WN, S::S, 1, false, WIDE>;
   auto kern = fp8_grouped_kernel<S::BM, S::BN, S::WM, S::WN, S::S, GATHER, WIDE>;
   static std::atomic<uint64_t> done{0};
   const hipError_t err = allow_lds(kern, T::kSmem, done);
@@ -252,7 +254,7 @@ hipError_t grouped_any(int32_t G, const int32_t* m_offsets, const int32_t* row_i
 template <typename S, bool WIDE>
 hipError_t wgrad(int32_t G, const int32_t* m_offsets, int64_t total_m, int64_t P, int64_t N,
                  int64_t K, Fp8Operand a, Fp8Operand b, Fp8Out y, hipStream_t stream) {
-  using T = Tile<S::BM, S::BN, S::WM, S::WN, S::S, true, WIDE>;
+  using T = Tile<S::BM, S::BN, S::WM, S::WN, S::S, 1, true, WIDE>;
   auto kern = fp8_wgrad_kernel<S::BM, S::BN, S::WM, S::WN, S::S, WIDE>;
   static std::atomic<uint64_t> done{0};
   const hipError_t err = allow_lds(kern, T::kSmem, done);

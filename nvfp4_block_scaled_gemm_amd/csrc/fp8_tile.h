@@ -90,9 +90,13 @@ struct TileOut {
     }
   }
 
-template <int BM, int BN, int WM, int WN, int STAGES, bool BROWS, bool WIDE>
+// KG: groups of WM x WN waves that take the blocks of K in turn, each with a
+// ring of its own, and add their sums at the end (in group order): small
+// tiles spend a step mostly on meeting and on LDS latency, so fewer steps with
+// two waves on each SIMD pay.
+template <int BM, int BN, int WM, int WN, int STAGES, int KG, bool BROWS, bool WIDE>
 struct Tile {
-  static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+  static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves * KG;
   static constexpr int TM = BM / WM, TN = BN / WN;
   static constexpr int FM = TM / 16, FN = TN / 16;
   static constexpr int kALoads = BM / 8 / kWaves, kBLoads = BN / 8 / kWaves;
@@ -101,7 +105,8 @@ struct Tile {
   static constexpr int kLoads = kALoads + kBLoads + kSLoads;  // per wave and stage
   static constexpr int kAOff = 0, kBOff = BM * kBlock, kSOff = (BM + BN) * kBlock;
   static constexpr int kStage = kSOff + (BM + BN) * 4;
-  static constexpr int kSmem = STAGES * kStage;
+  static constexpr int kSmem = KG * STAGES * kStage;
+  static_assert((KG - 1) * BM * BN * 4 <= kSmem, "the groups' sums fit the rings");
   static_assert(BM % (8 * kWaves) == 0 && BN % (8 * kWaves) == 0, "whole loads per wave");
   static_assert((kALoads & (kALoads - 1)) == 0 && (kBLoads & (kBLoads - 1)) == 0,
                 "the loads' row bits are disjoint");
@@ -120,12 +125,14 @@ struct Tile {
   // K: elements of the sum; ld: bytes between rows of both operands.
   template <bool GATHER>
   static __device__ __forceinline__ void run(const TileOperand& A, const TileOperand& B, uint32_t K,
-                                             uint32_t ld, const TileOut& out, uint8_t* smem) {
+                                             uint32_t ld, const TileOut& out, uint8_t* smem_all) {
     const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wave_all = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wave = wave_all % kWaves, kg = wave_all / kWaves;
+    uint8_t* const smem = smem_all + kg * STAGES * kStage;
     const int wm = wave / WN, wn = wave % WN;
     const int li = lane & 15, lg = lane >> 4;
-    const int nk = (int)((K + kBlock - 1) / kBlock);
+    const int nk = (int)((K + kBlock - 1) / kBlock), steps = (nk + KG - 1) / KG;
     // plain copies: a choice between two fields stays a choice of registers
     const uint8_t *const aq = A.q, *const bq = B.q;
     const float *const as = A.s, *const bs = B.s;
@@ -189,13 +196,14 @@ struct Tile {
     }
 
     // load number J (0 .. kLoads - 1) of stage s into ring slot `slot`; past
-    // the last stage every lane is out of range (zeros into a slot that is
+    // the last block every lane is out of range (zeros into a slot that is
     // not read again)
     auto load_one = [&](int s, int slot, auto jc) {
       constexpr int J = decltype(jc)::value;
       uint8_t* base = smem + slot * kStage;
-      const bool live = s < nk, cut = s == nk - 1;
-      const uint32_t soff = (uint32_t)s * kBlock;
+      const int kb = s * KG + kg;
+      const bool live = kb < nk, cut = kb == nk - 1;
+      const uint32_t soff = (uint32_t)kb * kBlock;
       if constexpr (J < kBLoads) {
         constexpr int i = J;
         load_lds16(make_rsrc(bq, live ? bq_bytes : 0u), base + kBOff + (wave * kBLoads + i) * 1024,
@@ -207,7 +215,7 @@ struct Tile {
       } else {
         constexpr int i = J - kBLoads - kALoads;
         const float* p = s_is_a[i] ? as : bs;
-        const int64_t at = (int64_t)max(min(s, nk - 1), 0) * (s_is_a[i] ? as_ld : bs_ld);
+        const int64_t at = (int64_t)max(min(kb, nk - 1), 0) * (s_is_a[i] ? as_ld : bs_ld);
         const uint32_t bytes = s_is_a[i] ? as_bytes : bs_bytes;
         load_lds4(make_rsrc(p + at, live ? bytes : 0u), base + kSOff + s_slot[i] * 256, s_off[i], 0);
       }
@@ -268,7 +276,7 @@ struct Tile {
       // no output of this wave exists (a group's last rows): it only loads
       // and meets the others, and leaves the matrix core to the wave beside it
       int slot = 0;
-      for (int s = 0; s < nk; ++s) {
+      for (int s = 0; s < steps; ++s) {
         static_for<kLoads - EARLY>([&](auto nc) {
           load_one(s + STAGES - 1, slot == 0 ? STAGES - 1 : slot - 1, std::integral_constant<int, EARLY + decltype(nc)::value>{});
         });
@@ -279,6 +287,7 @@ struct Tile {
       }
       wait_vmcnt<0>();
       workgroup_barrier();  // the others' turn to the ring for their outputs
+      if constexpr (KG > 1) workgroup_barrier();
       return;
     }
 #pragma unroll
@@ -286,7 +295,7 @@ struct Tile {
 #pragma unroll
     for (int h = 0; h < 2; ++h) ar[h] = read_a(smem, h);
     int slot = 0;
-    for (int s = 0; s < nk; ++s) {
+    for (int s = 0; s < steps; ++s) {
       const uint8_t* st = smem + slot * kStage;
       const int next = slot + 1 == STAGES ? 0 : slot + 1;
       const uint8_t* nst = smem + next * kStage;
@@ -367,9 +376,29 @@ struct Tile {
     // pieces, so that a store covers runs of TN elements instead of four.
     // (LDS accesses of one wave complete in order.)
     workgroup_barrier();
+    if constexpr (KG > 1) {
+      // the other groups' sums, each lane's own outputs
+      f32x4* sums = reinterpret_cast<f32x4*>(smem_all) + wave * (FM * FN * 64) + lane;
+      constexpr int kGroupSums = kWaves * FM * FN * 64;
+      if (kg > 0) {
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+          for (int j = 0; j < FM; ++j) sums[(kg - 1) * kGroupSums + (i * FM + j) * 64] = acc[i][j];
+      }
+      __syncthreads();
+      if (kg > 0) return;
+#pragma unroll
+      for (int g = 0; g < KG - 1; ++g)
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+          for (int j = 0; j < FM; ++j) acc[i][j] += sums[g * kGroupSums + (i * FM + j) * 64];
+    }
     constexpr int RS = TN + 4;  // floats per staged row; + 4 spreads the banks
-    static_assert(kWaves * 32 * RS * 4 <= kSmem, "staging fits the ring");
-    float* stage = reinterpret_cast<float*>(smem) + wave * 32 * RS;
+    constexpr int kStageAt = (KG - 1) * BM * BN;  // floats: behind the groups' sums
+    static_assert((kStageAt + kWaves * 32 * RS) * 4 <= kSmem, "staging fits the ring");
+    float* stage = reinterpret_cast<float*>(smem_all) + kStageAt + wave * 32 * RS;
     constexpr int LPR = TN / 8, RPI = 64 / LPR;  // lanes per row, rows per read
     constexpr int NP = 32 / RPI;
     // Whole aligned rows leave in 16-byte pieces, fp32 ones as two runs TN / 2
