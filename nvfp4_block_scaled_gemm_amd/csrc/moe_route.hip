@@ -467,7 +467,7 @@ __global__ __launch_bounds__(1024) void route_place_kernel(int T, int E, int k, 
     if (tid == 0) out.m_offsets[0] = 0;
   }
   // rows behind the last expert name no token
-  for (int64_t i = offset[E] + (int64_t)chunk * 1024 + tid; i < (int64_t)T * k; i += (int64_t)chunks * 1024)
+  for (int64_t i = max(offset[E], 0) + (int64_t)chunk * 1024 + tid; i < (int64_t)T * k; i += (int64_t)chunks * 1024)
     out.row_index[i] = -1;
   while (t < c1) {
     const int64_t i = (int64_t)t * k + slot;
@@ -477,10 +477,13 @@ __global__ __launch_bounds__(1024) void route_place_kernel(int T, int E, int k, 
       e_next = out.expert_index[(int64_t)tn * k + slot];
       p_next = out.pair_row[(int64_t)tn * k + slot];
     }
-    if (e >= 0) {
-      const int32_t at = offset[e] + lower[e] + p;
-      out.pair_row[i] = at;
-      out.row_index[at] = t;
+    if (e >= 0 && e < E) {
+      // inside the rows even if another call writes the same workspace
+      const uint32_t at = (uint32_t)(offset[e] + lower[e] + p);
+      if (at < (uint32_t)T * (uint32_t)k) {
+        out.pair_row[i] = (int32_t)at;
+        out.row_index[at] = t;
+      }
     }
     t = tn;
   }
