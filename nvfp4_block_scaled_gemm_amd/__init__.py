@@ -1,5 +1,7 @@
 """MI355X (gfx950) NVFP4 block-scaled GEMM: y = x . W^T with E2M1 operands,
-E4M3FN scales per 16 elements and fp32 per-tensor global scales.
+E4M3FN scales per 16 elements and fp32 per-tensor global scales; MXFP4 and
+FP8 (E4M3, one fp32 scale per 128) variants, grouped products for experts and
+the router that orders their tokens.
 
 The computation lives in ``libnvfp4.so`` (HIP kernels + C ABI, declared in
 ``include/nvfp4.h``); this package only marshals torch tensors into it.

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import typing
 
@@ -633,17 +634,16 @@ def _fp8_buffer(out, q_shape, s_shape, block_rows: int, x, dev: int) -> Fp8Packe
     return o
 
 
-def _fp8_buffers(layout: str, out, rows_shapes, cols_shapes, block_rows: int, x, dev: int):
-    """(rows operand or None, transposed operand or None) of a layout."""
+def _fp8_outs(layout: str, out):
+    """The caller's (rows, transposed) buffers for a layout, None where there
+    are none."""
     if layout == "rows":
-        return _fp8_buffer(out, *rows_shapes, block_rows, x, dev), None
+        return out, None
     if layout == "cols":
-        return None, _fp8_buffer(out, *cols_shapes, block_rows, x, dev)
+        return None, out
     _need(layout == "both", "layout: 'rows', 'cols' or 'both'")
     _need(out is None or len(out) == 2, "out: one operand per layout")
-    r, c = (None, None) if out is None else out
-    return (_fp8_buffer(r, *rows_shapes, block_rows, x, dev),
-            _fp8_buffer(c, *cols_shapes, block_rows, x, dev))
+    return (None, None) if out is None else out
 
 
 def _fp8_ptrs(rows, cols):
@@ -680,11 +680,15 @@ def _fp8_quantize(x, dt: int, block_rows: int, layout: str, out, dev: int):
     batch = lead[0] if lead else 1
     ld = _stride(x, cols, "x")
     _need(batch <= 1 or x.stride(0) == rows * ld, "x: matrices must follow each other")
-    rows_t, kb = -(-rows // 16) * 16, -(-cols // 128)
-    r, c = _fp8_buffers(
-        layout, out, ((*lead, rows, cols), (*lead, kb, -(-rows // block_rows))),
-        ((*lead, cols, rows_t), (*lead, -(-rows_t // 128), cols if block_rows == 1 else kb)),
-        block_rows, x, dev)
+    kb = -(-cols // 128)
+    out_r, out_c = _fp8_outs(layout, out)
+    r = c = None
+    if layout != "cols":
+        r = _fp8_buffer(out_r, (*lead, rows, cols), (*lead, kb, -(-rows // block_rows)), block_rows, x, dev)
+    if layout != "rows":
+        rows_t = -(-rows // 16) * 16
+        c = _fp8_buffer(out_c, (*lead, cols, rows_t),
+                        (*lead, -(-rows_t // 128), cols if block_rows == 1 else kb), block_rows, x, dev)
     st = nvfp4_fp8_quantize_raw(x.data_ptr(), dt, batch, rows, cols, ld, block_rows,
                                 *_fp8_ptrs(r, c), _stream(None, dev))
     if st != NVFP4_OK:
@@ -726,8 +730,12 @@ def nvfp4_fp8_grouped_quantize(x: torch.Tensor, m_offsets: torch.Tensor, layout:
     _need(G > 0 or total == 0, "m_offsets: no groups for the rows")
     P = nvfp4_fp8_grouped_columns(total, G)
     with contextlib.nullcontext() if _here(stream, dev) else _there(stream, dev):
-        r, c = _fp8_buffers(layout, out, ((total, cols), (-(-cols // 128), total)),
-                            ((cols, P), (P // 128, cols)), 1, x, dev)
+        out_r, out_c = _fp8_outs(layout, out)
+        r = c = None
+        if layout != "cols":
+            r = _fp8_buffer(out_r, (total, cols), (-(-cols // 128), total), 1, x, dev)
+        if layout != "rows":
+            c = _fp8_buffer(out_c, (cols, P), (P // 128, cols), 1, x, dev)
         st = nvfp4_fp8_grouped_quantize_raw(_ptr(x), _DT_IN[x.dtype], G, _ptr(m_offsets),
                                             None if row_index is None else _ptr(row_index), total,
                                             x_rows, cols, ld, *_fp8_ptrs(r, c), _stream(None, dev))
@@ -845,6 +853,7 @@ class MoeRoute(typing.NamedTuple):
     loss: torch.Tensor           # fp32 [1]
 
 
+@functools.lru_cache(maxsize=256)
 def nvfp4_moe_route_workspace_bytes(T: int, E: int) -> int:
     return int(load().nvfp4_moe_route_workspace_bytes(T, E))
 

@@ -42,13 +42,14 @@ __host__ __device__ inline int64_t chunk_tokens(int64_t T) {
   return c < 16 ? 16 : (c + 15) / 16 * 16;
 }
 
-// Order-keeping map of fp32 to unsigned; 0 for what is never chosen (-inf,
-// NaN), which no finite value maps to.
+// Order-keeping map of fp32 to unsigned.
 __device__ __forceinline__ uint32_t key_of(float x) {
   const uint32_t b = __float_as_uint(x);
-  if (!(x > -__builtin_inff())) return 0;
-  return b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
+// The image of -inf: what is not above it is never chosen.
+constexpr uint32_t kNever = 0x007FFFFFu;
+
 // Rotation inside each row of 16 lanes.
 template <int N>
 __device__ __forceinline__ uint32_t ror16(uint32_t v) {
@@ -126,23 +127,25 @@ template <int LPT, int NPL, int DT>
 __device__ __forceinline__ bool choose_by_keys(const float* v, int e0, int lg, int k, int32_t& got) {
   constexpr bool wide = DT == 0;
   constexpr uint32_t kExpert = LPT * NPL - 1;  // the expert's bits of a key
+  constexpr uint32_t kNone = (kNever >> 1) | kExpert;  // keys up to here: an expert at -inf
   uint32_t key[NPL], g = 0;
 #pragma unroll
   for (int i = 0; i < NPL; ++i) {
-    const uint32_t b = key_of(v[i]);  // 0: never chosen; any other stays above kExpert
-    key[i] = b == 0 ? 0u : (((b >> 1) & ~kExpert) | (kExpert - (uint32_t)(e0 + i)));
+    key[i] = ((key_of(v[i]) >> 1) & ~kExpert) | (kExpert - (uint32_t)(e0 + i));
     g = max(g, key[i]);
   }
   g = group_max<LPT>(g);
   bool same = false;
   for (int j = 0; j < k; ++j) {
-    if (lg == j && g != 0) got = (int32_t)(kExpert - (g & kExpert));
+    if (lg == j && g > kNone) got = (int32_t)(kExpert - (g & kExpert));
     if (j == k - 1 && !wide) break;  // fp32 looks at one more
     uint32_t m = key[0] - g;
 #pragma unroll
     for (int i = 1; i < NPL; ++i) m = max(m, key[i] - g);
-    const uint32_t next = g != 0 ? group_max<LPT>(m) + g : 0u;
-    same = same || (g != 0 && next != 0 && ((next ^ g) & ~kExpert) == 0);
+    m = group_max<LPT>(m);
+    // no key below the last one: the search is over
+    const uint32_t next = (int32_t)m < 0 ? m + g : 0u;
+    same = same || (next > kNone && ((next ^ g) & ~kExpert) == 0);
     g = next;
   }
   return same && wide;
@@ -153,9 +156,12 @@ template <int LPT, int NPL>
 __device__ __forceinline__ int32_t choose_exactly(const float (&v)[NPL], int e0, int lg, int grp,
                                                   int k) {
   int32_t got = -1;
-  uint32_t key[NPL];
+  uint32_t key[NPL];  // 0: never chosen, or chosen already
 #pragma unroll
-  for (int i = 0; i < NPL; ++i) key[i] = key_of(v[i]);
+  for (int i = 0; i < NPL; ++i) {
+    key[i] = key_of(v[i]);
+    if (key[i] <= kNever) key[i] = 0;
+  }
   for (int j = 0; j < k; ++j) {
     uint32_t m = key[0];
 #pragma unroll
@@ -265,7 +271,7 @@ __global__ __launch_bounds__(1024) void route_choose_kernel(
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < NPL; ++i) {
-        v[i] = active ? __expf(v[i] - top) : 0.f;
+        v[i] = __expf(v[i] - top);  // an inactive row's -inf gives 0
         sum += v[i];
       }
       sum = group_sum<LPT>(sum);
@@ -529,7 +535,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(
     float sum = 0.f, dot = 0.f;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
-      v[i] = active ? __expf(v[i] - top) : 0.f;
+      v[i] = __expf(v[i] - top);  // an inactive row's -inf gives 0
       sum += v[i];
     }
     sum = group_sum<LPT>(sum);
