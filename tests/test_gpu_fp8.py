@@ -244,6 +244,22 @@ def test_gemm_empty():
     assert nv.nvfp4_fp8_gemm(z, w).shape == (0, 8)
 
 
+def test_gemm_past_4_gib():
+    """An activation operand past 2^32 bytes, and the same rows read through an
+    index below 2^31; rows on both sides of the 2^31 and 2^32 byte offsets."""
+    M, N, K = 300000, 72, 16384
+    g = torch.Generator(device=DEV).manual_seed(5)
+    q = torch.empty(M, K, dtype=torch.uint8, device=DEV)
+    for i in range(0, M, 50000):
+        q[i:i + 50000] = torch.randint(0, 120, (50000, K), dtype=torch.uint8, device=DEV, generator=g)
+    s = torch.rand(K // 128, M, device=DEV, generator=g)
+    b = rand_operand(np.random.default_rng(5), N, K, 128)
+    note("fp8 gemm past 4 GiB")
+    y = nv.nvfp4_fp8_gemm((q.view(torch.float8_e4m3fn), s), to_gpu(b), "bf16")
+    rows = [0, 131071, 131072, 131073, 262143, 262144, 262145, M - 1]
+    close(y[rows], (np_(q[rows]), np_(s[:, rows])), b, 128, "bf16")
+
+
 GROUPS = [[5], [0, 3, 0, 40, 1], [16] * 9, [130, 0, 257, 64, 1], [1, 2] * 40, [0, 0, 700], [33, 64, 65, 0]]
 
 
