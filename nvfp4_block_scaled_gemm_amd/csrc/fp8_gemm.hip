@@ -119,7 +119,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_wgrad_kernel(
   const int tiles = tiles_m * tiles_n, per = (tiles + kXcds - 1) / kXcds;
   const int e = blockIdx.x / kXcds / per, in = blockIdx.x % kXcds * per + blockIdx.x / kXcds % per;
   if (in >= tiles) return;
-  const int64_t m0 = (int64_t)(in % tiles_m) * BM, n0 = (int64_t)(in / tiles_m) * BN;
+  // along the rows of dW first: neighbours write neighbouring columns (down
+  // the columns first: 1125 instead of 1086 us for 64 x 4096 x 2048 fp32)
+  const int64_t m0 = (int64_t)(in / tiles_n) * BM, n0 = (int64_t)(in % tiles_n) * BN;
   const int lane = threadIdx.x & 63;
   uint32_t blocks = 0;  // blocks of the experts before e
   for (int i = lane; i < e; i += 64) blocks += (uint32_t)((segment(offsets, i, total_m).n + kBlock - 1) / kBlock);
