@@ -279,10 +279,7 @@ hipError_t by_width(const Fp8Out& y, F&& f) {
 
 hipError_t launch_fp8_gemm(int64_t M, int64_t N, int64_t K, Fp8Operand a, Fp8Operand b,
                            int b_block_rows, Fp8Out y, hipStream_t stream) {
-  // up to 32 rows the weights' stream is all that counts (M = 32, N = K =
-  // 8192: 21 us streamed, 31 in 64 x 64 tiles; from 33 rows on the stream
-  // kernel re-reads A too often: M = 64 29 us, tiles 23)
-  if (M <= 32) return launch_fp8_stream(M, N, K, a, b, b_block_rows, y, stream);
+  if (fp8_streams(M, N)) return launch_fp8_stream(M, N, K, a, b, b_block_rows, y, stream);
   return by_width(y, [&](auto wide) {
     constexpr bool W = decltype(wide)::value;
     return b_block_rows == 1 ? dense_any<true, W>(M, N, K, a, b, y, stream)

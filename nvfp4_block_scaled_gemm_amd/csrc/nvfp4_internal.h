@@ -145,7 +145,8 @@ hipError_t launch_fp8_grouped_quantize(const void* x, int dtype, int32_t G,
 // fp8_gemm.hip: K % 16 == 0, K <= 2^22, 16-byte aligned q.
 hipError_t launch_fp8_gemm(int64_t M, int64_t N, int64_t K, Fp8Operand a, Fp8Operand b,
                            int b_block_rows, Fp8Out y, hipStream_t stream);
-// fp8_stream.hip: the same for few rows (M <= 32).
+// fp8_stream.hip: the same for few rows or few outputs, and which those are.
+bool fp8_streams(int64_t M, int64_t N);
 hipError_t launch_fp8_stream(int64_t M, int64_t N, int64_t K, Fp8Operand a, Fp8Operand b,
                              int b_block_rows, Fp8Out y, hipStream_t stream);
 // row_index != nullptr: a_rows * K < 2^31

@@ -149,7 +149,8 @@ def close(y, a, b, block_rows, out, rows=None, add=None):
 
 SHAPES = [(1, 1, 16), (1, 300, 128), (2, 17, 144), (3, 256, 1024), (5, 8, 2064), (16, 128, 256), (17, 200, 512),
           (31, 130, 400), (33, 1000, 640), (48, 64, 8192), (64, 96, 272), (65, 129, 1040), (100, 513, 384),
-          (128, 128, 128), (130, 4100, 256), (200, 333, 1552), (257, 640, 112)]
+          (128, 128, 128), (130, 4100, 256), (200, 333, 1552), (257, 640, 112), (70, 8300, 2064), (600, 1000, 1040),
+          (1000, 520, 8192)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
@@ -176,8 +177,21 @@ def test_gemm_many_tiles(M, N, K, block_rows):
     close(y, a, b, block_rows, "f32", rows=rows)
 
 
+@pytest.mark.parametrize("M,N,K", [(20, 16400, 272), (90, 16400, 144), (512, 4104, 272), (1000, 8200, 144),
+                                   (1000, 4500, 272), (2500, 8200, 144)])
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_gemm_many_tiles_bf16(M, N, K, block_rows):
+    """The 8-bit products' tile shapes, ragged edges; sampled rows."""
+    rng = np.random.default_rng(M + N + K)
+    a, b = rand_operand(rng, M, K), rand_operand(rng, N, K, block_rows)
+    note(f"fp8 gemm {M}x{N}x{K} block_rows {block_rows} bf16 (many tiles)")
+    y = nv.nvfp4_fp8_gemm(to_gpu(a), to_gpu(b), "bf16")
+    rows = np.unique(np.concatenate([[0, M // 2, M - 1], rng.choice(M, min(M, 24), replace=False)]))
+    close(y, a, b, block_rows, "bf16", rows=rows)
+
+
 @pytest.mark.parametrize("M,N,K,block_rows", [(1, 512, 512, 128), (40, 300, 272, 1), (300, 257, 384, 1),
-                                              (300, 257, 384, 128)])
+                                              (300, 257, 384, 128), (600, 1500, 400, 1), (70, 8300, 272, 128)])
 def test_gemm_accumulates(M, N, K, block_rows):
     rng = np.random.default_rng(M + N)
     a, b = rand_operand(rng, M, K), rand_operand(rng, N, K, block_rows)
@@ -188,13 +202,13 @@ def test_gemm_accumulates(M, N, K, block_rows):
     close(y, a, b, block_rows, "f32", add=y0.astype(np.float64))
 
 
-@pytest.mark.parametrize("M", [1, 20, 200])
+@pytest.mark.parametrize("M,N", [(1, 130), (20, 130), (200, 130), (2100, 130)])
 @pytest.mark.parametrize("out,ld,shift", [("bf16", 136, 0), ("bf16", 133, 1), ("f32", 132, 0), ("f32", 131, 3)])
-def test_gemm_writes_only_its_view(M, out, ld, shift):
+def test_gemm_writes_only_its_view(M, N, out, ld, shift):
     """Row strides and bases that allow 16-byte stores and ones that do not;
     the bytes around y stay."""
     rng = np.random.default_rng(ld)
-    N, K = 130, 256
+    K = 256
     a, b = rand_operand(rng, M, K), rand_operand(rng, N, K, 128)
     dt = torch.bfloat16 if out == "bf16" else torch.float32
     buf = torch.full((M * ld + 64,), 7.0, dtype=dt, device=DEV)
@@ -207,7 +221,7 @@ def test_gemm_writes_only_its_view(M, out, ld, shift):
     assert bool((rest == 7.0).all())
 
 
-@pytest.mark.parametrize("M", [3, 40, 300])
+@pytest.mark.parametrize("M", [3, 40, 300, 1100])
 def test_gemm_exact_codes_and_nan_scales(M):
     """Every finite code against a unit row: exact; a NaN scale marks its row
     (or column block) and no other."""
@@ -288,6 +302,33 @@ def test_grouped(counts, N, K, gather, out):
         close(torch.from_numpy(y[lo:hi]), (q, s), (b[0][e], b[1][e]), 128, out)
 
 
+@pytest.mark.parametrize("counts", [[0, 400, 3, 130, 128, 250, 289, 100],
+                                    [0, 1000, 300, 257, 1, 511, 700, 256, 900, 640, 5, 833, 720, 610, 512, 900]],
+                         ids=lambda c: f"G{len(c)}t{sum(c)}")
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_grouped_many_tiles(counts, gather, out):
+    """Rows enough for the larger tiles, which few columns never take; each
+    expert's edge rows and some more."""
+    N, K = 4104, 144
+    rng = np.random.default_rng(sum(counts))
+    off = wl.ragged_offsets(counts)
+    total, G = int(off[-1]), len(counts)
+    a_rows = 1111 if gather else total
+    a, b = rand_operand(rng, a_rows, K), rand_operand(rng, N, K, 128, (G,))
+    idx = rng.integers(0, a_rows, total).astype(np.int32)
+    note(f"fp8 grouped {G} groups {total} rows N {N} K {K} gather {gather} {out} (many tiles)")
+    y = nv.nvfp4_fp8_grouped_gemm(off.to(DEV), total, to_gpu(a), to_gpu(b), out,
+                                  row_index=torch.from_numpy(idx).to(DEV) if gather else None)
+    for e in range(G):
+        lo, hi = int(off[e]), int(off[e + 1])
+        if lo == hi:
+            continue
+        rows = np.unique(np.concatenate([[lo, hi - 1], rng.integers(lo, hi, 10)]))
+        src = idx[rows] if gather else rows
+        close(y[rows], (a[0][src], a[1][:, src]), (b[0][e], b[1][e]), 128, out)
+
+
 def test_grouped_leaves_rows_of_no_group():
     rng = np.random.default_rng(4)
     a, b = rand_operand(rng, 50, 128), rand_operand(rng, 40, 128, 128, (2,))
@@ -353,6 +394,28 @@ def test_wgrad(counts, N, K, out, add):
         else:
             close(torch.from_numpy(dw[e]), part(aq, sa), part(bq, sb), 1, out,
                   add=dw0[e].double().numpy() if add else None)
+        at += n
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_wgrad_many_tiles(out):
+    counts, N, K = [300, 0, 129, 5], 2032, 2000
+    off = wl.ragged_offsets(counts)
+    total = int(off[-1])
+    note(f"fp8 wgrad {counts} N {N} K {K} {out} (many tiles)")
+    a = nv.nvfp4_fp8_grouped_quantize(values(total, N, 4, "fp32").to(DEV), off.to(DEV))
+    b = nv.nvfp4_fp8_grouped_quantize(values(total, K, 5, "bf16").to(DEV), off.to(DEV))
+    dw = nv.nvfp4_fp8_grouped_wgrad(off.to(DEV), total, a, b, out)
+    aq, sa, bq, sb = bytes_of(a[0]), np_(a[1]), bytes_of(b[0]), np_(b[1])
+    at = 0
+    for e, c in enumerate(counts):
+        n = -(-c // 128) * 128
+        part = lambda q, s: (q[:, at:at + n], s[at // 128:(at + n) // 128])  # noqa: E731
+        if c == 0:
+            assert bool((dw[e] == 0).all())
+        else:
+            rows = np.arange(e, N, 37)
+            close(dw[e], part(aq, sa), part(bq, sb), 1, out, rows=rows)
         at += n
 
 
