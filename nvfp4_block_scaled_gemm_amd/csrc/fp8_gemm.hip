@@ -179,10 +179,17 @@ hipError_t dense(int64_t M, int64_t N, int64_t K, Fp8Operand a, Fp8Operand b, Fp
 // Time of a shape in units of 0.01 us per block of K, from the tiles that the
 // busiest of 256 CUs gets: t1 for one tile alone on a CU, t2 for two (shapes
 // of which one fits a CU: twice t1).
-int64_t shape_cost(int64_t M, int64_t N, int64_t bm, int64_t bn, int64_t t1, int64_t t2) {
-  const int64_t tiles = ((M + bm - 1) / bm) * ((N + bn - 1) / bn);
+int64_t tiles_cost(int64_t tiles, int64_t t1, int64_t t2) {
   const int64_t n = (tiles + 255) / 256;
   return n / 2 * t2 + n % 2 * t1;
+}
+
+int64_t tiles_of(int64_t rows, int64_t cols, int64_t bm, int64_t bn) {
+  return ((rows + bm - 1) / bm) * ((cols + bn - 1) / bn);
+}
+
+int64_t shape_cost(int64_t M, int64_t N, int64_t bm, int64_t bn, int64_t t1, int64_t t2) {
+  return tiles_cost(tiles_of(M, N, bm, bn), t1, t2);
 }
 
 // The shape with the least expected time.  Measured (us per block of 128,
@@ -242,13 +249,28 @@ template <bool GATHER, bool WIDE>
 hipError_t grouped_any(int32_t G, const int32_t* m_offsets, const int32_t* row_index,
                        int64_t total_m, int64_t a_rows, int64_t N, int64_t K, Fp8Operand a,
                        Fp8Operand b, Fp8Out y, hipStream_t stream) {
-  // the counts are on the device: the shape goes by the mean
-  const int64_t mean = total_m / G;
+  // The counts are on the device.  Expected tile rows: one for every expert
+  // that can have rows, or the rows' worth and half a tile more for each; then
+  // the least expected time, with the dense figures and 0.60 / 0.97 for
+  // 64 x 128, wide 0.90 / 1.40.  Measured in us, 64 x 128 / 128 x 128 /
+  // 256 x 256 (K = 2048 but for the second): 256 experts of 16 rows, N = 4096
+  // 383 / 422 / 433; 8 of 150, N = K = 4096 50 / 39 / 60; 64 of 64, N = 2048
+  // 60 / 53 / 59; 64 of 128 96 / 89 / 78; 128 of 512, N = 4096 1088 / 840 / 686.
+  // Wide, the first two shapes: 32 of 19, N = 1024 26 / 32; 8 of 150, N = K =
+  // 4096 75 / 62; 64 of 128, N = 2048 121 / 116; 128 of 512 1530 / 1254.
+  const int64_t live = G < total_m ? G : total_m;
+  auto cost = [&](int64_t bm, int64_t bn, int64_t t1, int64_t t2) {
+    const int64_t rows = total_m / bm + live / 2;
+    return tiles_cost((rows > live ? rows : live) * ((N + bn - 1) / bn), t1, t2);
+  };
+  const int64_t small = WIDE ? cost(64, 128, 90, 140) : cost(64, 128, 60, 97);
+  const int64_t middle = WIDE ? cost(128, 128, 126, 206) : cost(128, 128, 90, 122);
   if constexpr (!WIDE) {
-    if (mean > 128)
+    const int64_t large = cost(256, 256, 170, 340);
+    if (large < small && large < middle)
       return grouped<S256x256, GATHER, WIDE>(G, m_offsets, row_index, total_m, a_rows, N, K, a, b, y, stream);
   }
-  if (mean > 64)
+  if (middle < small)
     return grouped<S128x128, GATHER, WIDE>(G, m_offsets, row_index, total_m, a_rows, N, K, a, b, y, stream);
   return grouped<S64x128, GATHER, WIDE>(G, m_offsets, row_index, total_m, a_rows, N, K, a, b, y, stream);
 }
@@ -302,7 +324,13 @@ hipError_t launch_fp8_wgrad(int32_t G, const int32_t* m_offsets, int64_t total_m
                             int64_t N, int64_t K, Fp8Operand a, Fp8Operand b, Fp8Out y,
                             hipStream_t stream) {
   if (y.dtype == 0) return wgrad<S128x128, true>(G, m_offsets, total_m, P, N, K, a, b, y, stream);
-  return wgrad<S256x256, false>(G, m_offsets, total_m, P, N, K, a, b, y, stream);
+  // the dense rule's figures: 128 x 128 where 256 x 256 leaves CUs idle (bf16,
+  // 32 experts of 256 x 384 11.8 us instead of 16.8, 8 of 1024 x 1024 33
+  // instead of 40; 16 of 2048 x 1024 46 instead of 42)
+  const int64_t large = tiles_cost(G * tiles_of(N, K, 256, 256), 170, 340);
+  const int64_t middle = tiles_cost(G * tiles_of(N, K, 128, 128), 90, 122);
+  return middle < large ? wgrad<S128x128, false>(G, m_offsets, total_m, P, N, K, a, b, y, stream)
+                        : wgrad<S256x256, false>(G, m_offsets, total_m, P, N, K, a, b, y, stream);
 }
 
 }  // namespace nvfp4
