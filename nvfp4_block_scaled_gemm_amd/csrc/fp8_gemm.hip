@@ -312,6 +312,8 @@ hipError_t launch_fp8_gemm(int64_t M, int64_t N, int64_t K, Fp8Operand a, Fp8Ope
 hipError_t launch_fp8_grouped(int32_t G, const int32_t* m_offsets, const int32_t* row_index,
                               int64_t total_m, int64_t a_rows, int64_t N, int64_t K, Fp8Operand a,
                               Fp8Operand b, Fp8Out y, hipStream_t stream) {
+  if (fp8_grouped_streams(G, total_m, N, K))
+    return launch_fp8_grouped_stream(G, m_offsets, row_index, total_m, a_rows, N, K, a, b, y, stream);
   return by_width(y, [&](auto wide) {
     constexpr bool W = decltype(wide)::value;
     return row_index != nullptr

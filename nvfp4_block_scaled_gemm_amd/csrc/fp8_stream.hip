@@ -33,25 +33,36 @@ __device__ __forceinline__ i32x8 load_fragment(__amdgpu_buffer_rsrc_t r, uint32_
   return join(__builtin_bit_cast(u32x4, a), __builtin_bit_cast(u32x4, b));
 }
 
+// Rows of A that a workgroup multiplies: lane li of fragment j takes row
+// 16 j + li, whose bytes and scale are at the offsets (kNoRow: zeros).
+template <int FM>
+struct StreamRows {
+  const uint8_t* q;
+  const float* s;
+  int64_t s_ld;
+  uint32_t q_bytes, s_bytes;
+  uint32_t q_off[FM], s_off[FM];
+};
+
+// BM x BN outputs from rn rows of B at bq (scales of block 0 at bs, s_ld
+// apart) and the rows of A.
 template <int BM, int BN, int UNROLL, int WAVES, bool BROWS, bool WIDE>
-__global__ __launch_bounds__(64 * WAVES) void fp8_stream_kernel(int64_t M, int64_t N, int64_t K,
-                                                                Fp8Operand a, Fp8Operand b, Fp8Out y) {
+__device__ __forceinline__ void stream_outputs(const StreamRows<BM / 16>& A, const uint8_t* bq,
+                                               const float* bs, int64_t bs_ld, int rn, int64_t K,
+                                               const TileOut& out) {
   constexpr int FM = BM / 16, FN = BN / 16;
   __shared__ __attribute__((aligned(16))) float part[WAVES][BM][BN];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 15, lg = lane >> 4;
-  const int64_t tiles_n = (N + BN - 1) / BN;
-  const int64_t m0 = blockIdx.x / tiles_n * BM, n0 = blockIdx.x % tiles_n * BN;
-  const int rm = (int)min((int64_t)BM, M - m0), rn = (int)min((int64_t)BN, N - n0);
   const int nk = (int)((K + kBlock - 1) / kBlock);
   const uint32_t ld = (uint32_t)K, end = (uint32_t)K - (uint32_t)(nk - 1) * kBlock;
   const bool lo_past = (uint32_t)lg * 16 >= end, hi_past = (uint32_t)(lg + 4) * 16 >= end;
-  const auto ra = make_rsrc(a.q + m0 * K, (uint32_t)rm * ld);
-  const auto rb = make_rsrc(b.q + n0 * K, (uint32_t)rn * ld);
+  const auto ra = make_rsrc(A.q, A.q_bytes);
+  const auto rb = make_rsrc(bq, (uint32_t)rn * ld);
   uint32_t a_off[FM], b_off[FN];
 #pragma unroll
-  for (int j = 0; j < FM; ++j) a_off[j] = (uint32_t)(16 * j + li) * ld + lg * 16;
+  for (int j = 0; j < FM; ++j) a_off[j] = A.q_off[j] + lg * 16;
 #pragma unroll
   for (int i = 0; i < FN; ++i) {
     // two fragments give a lane eight neighbouring columns (one: four)
@@ -63,7 +74,6 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_stream_kernel(int64_t M, int64
   for (int i = 0; i < FN; ++i)
 #pragma unroll
     for (int j = 0; j < FM; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int64_t nb = (N + kBlock - 1) / kBlock;
 
   for (int k0 = wave; k0 < nk; k0 += WAVES * UNROLL) {
     i32x8 bf[UNROLL][FN], af[UNROLL][FM];
@@ -85,15 +95,15 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_stream_kernel(int64_t M, int64
       const bool none = kb >= nk, cut = kb == nk - 1;
       const uint32_t soff = (uint32_t)kb * kBlock;
       const int64_t at = none ? 0 : kb;
-      const auto rsa = make_rsrc(a.s + at * M + m0, none ? 0u : (uint32_t)rm * 4);
+      const auto rsa = make_rsrc(A.s + at * A.s_ld, none ? 0u : A.s_bytes);
 #pragma unroll
       for (int j = 0; j < FM; ++j) {
         af[u][j] = load_fragment(ra, none || (cut && lo_past) ? kNoRow : a_off[j],
                                  none || (cut && hi_past) ? kNoRow : a_off[j] + 64, soff);
-        sa[u][j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rsa, (uint32_t)(16 * j + li) * 4, 0, 0));
+        sa[u][j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rsa, A.s_off[j], 0, 0));
       }
       if constexpr (BROWS) {
-        const auto rsb = make_rsrc(b.s + at * N + n0, none ? 0u : (uint32_t)rn * 4);
+        const auto rsb = make_rsrc(bs + at * bs_ld, none ? 0u : (uint32_t)rn * 4);
 #pragma unroll
         for (int i = 0; i < FN; ++i) {
           const int n = FN == 1 ? 4 * lg : 32 * (i >> 1) + 8 * lg + 4 * (i & 1);
@@ -102,7 +112,7 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_stream_kernel(int64_t M, int64
             sb[u][i][e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rsb, (uint32_t)(n + e) * 4, 0, 0));
         }
       } else {
-        sb[u][0][0] = b.s[at * nb + n0 / kBlock];
+        sb[u][0][0] = bs[at * bs_ld];
       }
     }
 #pragma unroll
@@ -134,10 +144,9 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_stream_kernel(int64_t M, int64
       *reinterpret_cast<f32x4*>(&part[wave][16 * j + li][n]) = acc[i][j];
     }
   __syncthreads();
-  const TileOut out{(uint8_t*)y.y + (m0 * y.ld + n0) * (y.dtype == 0 ? 4 : 2), y.ld, rm, rn, y.dtype, y.add, y.vec};
   for (int t = tid; t < BM * BN / 8; t += 64 * WAVES) {
     const int m = t / (BN / 8), n = t % (BN / 8) * 8;
-    if (m >= rm || n >= rn) continue;
+    if (m >= out.m || n >= out.n) continue;
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = 0.f;
@@ -153,6 +162,87 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_stream_kernel(int64_t M, int64
     }
     store8(out, m, n, v);
   }
+}
+
+__device__ __forceinline__ TileOut out_of(const Fp8Out& y, int64_t m0, int64_t n0, int m, int n) {
+  return {(uint8_t*)y.y + (m0 * y.ld + n0) * (y.dtype == 0 ? 4 : 2), y.ld, m, n, y.dtype, y.add, y.vec};
+}
+
+// Rows m0 .. m0 + n of a K-block-major operand with `rows` rows.
+template <int FM>
+__device__ __forceinline__ StreamRows<FM> rows_from(const Fp8Operand& a, int64_t rows, int64_t m0,
+                                                    int n, int64_t K) {
+  StreamRows<FM> r{a.q + m0 * K, a.s + m0, rows, (uint32_t)n * (uint32_t)K, (uint32_t)n * 4, {}, {}};
+#pragma unroll
+  for (int j = 0; j < FM; ++j) {
+    const uint32_t row = 16 * j + (threadIdx.x & 15);
+    r.q_off[j] = row * (uint32_t)K;
+    r.s_off[j] = row * 4;
+  }
+  return r;
+}
+
+template <int BM, int BN, int UNROLL, int WAVES, bool BROWS, bool WIDE>
+__global__ __launch_bounds__(64 * WAVES) void fp8_stream_kernel(int64_t M, int64_t N, int64_t K,
+                                                                Fp8Operand a, Fp8Operand b, Fp8Out y) {
+  const int64_t tiles_n = (N + BN - 1) / BN;
+  const int64_t m0 = blockIdx.x / tiles_n * BM, n0 = blockIdx.x % tiles_n * BN;
+  const int rm = (int)min((int64_t)BM, M - m0), rn = (int)min((int64_t)BN, N - n0);
+  const int64_t s_ld = BROWS ? N : (N + kBlock - 1) / kBlock;
+  stream_outputs<BM, BN, UNROLL, WAVES, BROWS, WIDE>(
+      rows_from<BM / 16>(a, M, m0, rm, K), b.q + n0 * K, b.s + (BROWS ? n0 : n0 / kBlock), s_ld, rn, K,
+      out_of(y, m0, n0, rm, rn));
+}
+
+// Experts' products of few rows: the workgroup's (expert, tile column, tile
+// row) in a list that is known on the device only, 64 experts' running counts
+// in a wave's lanes at a time.  Eight tile columns of an expert's rows in
+// turn, so that the rows of one column share its XCD's L2.
+template <int BM, int BN, int UNROLL, int WAVES, bool GATHER, bool WIDE>
+__global__ __launch_bounds__(64 * WAVES) void fp8_grouped_stream_kernel(
+    int G, const int32_t* __restrict__ offsets, const int32_t* __restrict__ row_index,
+    int64_t total_m, int64_t a_rows, int64_t N, int64_t K, Fp8Operand a, Fp8Operand b, Fp8Out y) {
+  const int lane = threadIdx.x & 63;
+  const int64_t tiles_n = (N + BN - 1) / BN, nb = (N + kBlock - 1) / kBlock, kb = (K + kBlock - 1) / kBlock;
+  int64_t v = blockIdx.x;
+  int e0 = 0;
+  Segment sg;
+  uint32_t upto, all;
+  for (;;) {
+    sg = e0 + lane < G ? segment(offsets, e0 + lane, total_m) : Segment{0, 0};
+    upto = wave_scan((uint32_t)((sg.n + BM - 1) / BM));
+    all = __builtin_amdgcn_readlane(upto, 63);
+    if (v < all * tiles_n) break;
+    v -= all * tiles_n;
+    e0 += 64;
+    if (e0 >= G) return;
+  }
+  // first lane whose running count passes the tile
+  const int l = __builtin_ctzll(__ballot((int64_t)upto * tiles_n > v));
+  const int64_t start = l == 0 ? 0 : (int64_t)__builtin_amdgcn_readlane(upto, l - 1);
+  const int32_t lo = __builtin_amdgcn_readlane(sg.lo, l), n = __builtin_amdgcn_readlane(sg.n, l);
+  const int32_t te = (n + BM - 1) / BM;
+  const int64_t w = v - start * tiles_n, eight = w / (8 * te) * 8;
+  const int32_t in = (int32_t)(w - eight * te), cols = (int32_t)min(tiles_n - eight, (int64_t)8);
+  const int32_t tm = in / cols;
+  const int64_t e = e0 + l, m0 = lo + (int64_t)tm * BM, n0 = (eight + in % cols) * BN;
+  const int rm = min(BM, n - tm * BM), rn = (int)min((int64_t)BN, N - n0);
+  StreamRows<BM / 16> A;
+  if constexpr (GATHER) {
+    A = {a.q, a.s, a_rows, (uint32_t)(a_rows * K), (uint32_t)a_rows * 4, {}, {}};
+#pragma unroll
+    for (int j = 0; j < BM / 16; ++j) {
+      const int r = 16 * j + (lane & 15);
+      const int32_t row = r < rm ? row_index[m0 + r] : -1;
+      const bool ok = row >= 0 && row < a_rows;
+      A.q_off[j] = ok ? (uint32_t)row * (uint32_t)K : kNoRow;
+      A.s_off[j] = ok ? (uint32_t)row * 4 : kNoRow;
+    }
+  } else {
+    A = rows_from<BM / 16>(a, total_m, m0, rm, K);
+  }
+  stream_outputs<BM, BN, UNROLL, WAVES, false, WIDE>(A, b.q + (e * N + n0) * K, b.s + e * kb * nb + n0 / kBlock,
+                                                     nb, rn, K, out_of(y, m0, n0, rm, rn));
 }
 
 // Workgroups of a tile size.
@@ -193,7 +283,71 @@ hipError_t stream_rows(int64_t M, int64_t N, int64_t K, Fp8Operand a, Fp8Operand
   return stream_cfg<32, 32, 2, 8, BROWS, WIDE>(M, N, K, a, b, y, stream);
 }
 
+// Outputs per workgroup of the experts' product, from the workgroups to be
+// expected: one tile row for every expert that can have rows, or the rows'
+// worth and half a tile more for each.  16 x 16 while they do not fill the
+// card (2 experts with a row each, N = 1024, K = 4096: 6.2 us, 16 x 32 7.4,
+// 64 x 128 in the ring 16.4); 16 x 32 where one tile holds an expert's rows
+// and K is long enough for what a workgroup costs (us, this and the ring: 8
+// experts of 1 row, N = 4096, K = 2048 16.0 / 23.0; 2 of 1, 4096 x 14336 20.4 /
+// 94.7; 64 of 1, 1536 x 4096 60 / 83; but 32 of 1, 4096 x 2048 51.9 / 48.8, 32
+// of 4, 4096 x 1024 29.7 / 23.5); 32 x 32 for some more rows (8 of 16, 1024 x
+// 4096 10.9 / 31.0; 8 of 12, 4096 x 4096 29.1 / 31.2; 32 of 16, 1024 x 2048
+// 18.0 / 18.7; but 32 of 32, 1024 x 2048 28.6 / 19.9).
+enum GroupedOutputs { kTiles, kRows16x16, kRows16x32, kRows32x32 };
+GroupedOutputs grouped_outputs(int64_t G, int64_t total_m, int64_t N, int64_t K) {
+  const int64_t live = G < total_m ? G : total_m;
+  const int64_t more = total_m / 16 + live / 2, rows = more > live ? more : live;
+  const int64_t more32 = total_m / 32 + live / 2, rows32 = more32 > live ? more32 : live;
+  const int64_t n16 = (N + 15) / 16, n32 = (N + 31) / 32;
+  if (rows * n16 <= kCUs) return kRows16x16;
+  if (rows * n32 <= kCUs || (more <= live && 2 * rows * n32 <= 3 * K)) return kRows16x32;
+  return rows32 * n32 <= 4 * kCUs && 2 * rows32 * n32 <= K ? kRows32x32 : kTiles;
+}
+
+template <int BM, int BN, int UNROLL, int WAVES, bool GATHER, bool WIDE>
+hipError_t grouped_cfg(int32_t G, const int32_t* m_offsets, const int32_t* row_index,
+                       int64_t total_m, int64_t a_rows, int64_t N, int64_t K, Fp8Operand a,
+                       Fp8Operand b, Fp8Out y, hipStream_t stream) {
+  // an expert ends at most one tile that is not full
+  const int64_t tiles = (total_m / BM + (G < total_m ? G : total_m)) * ((N + BN - 1) / BN);
+  if (tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
+  fp8_grouped_stream_kernel<BM, BN, UNROLL, WAVES, GATHER, WIDE>
+      <<<(unsigned)tiles, 64 * WAVES, 0, stream>>>(G, m_offsets, row_index, total_m, a_rows, N, K, a, b, y);
+  return hipGetLastError();
+}
+
+template <bool GATHER, bool WIDE>
+hipError_t grouped_rows(int32_t G, const int32_t* m_offsets, const int32_t* row_index,
+                        int64_t total_m, int64_t a_rows, int64_t N, int64_t K, Fp8Operand a,
+                        Fp8Operand b, Fp8Out y, hipStream_t stream) {
+  switch (grouped_outputs(G, total_m, N, K)) {
+    case kRows16x16:
+      return grouped_cfg<16, 16, 4, 8, GATHER, WIDE>(G, m_offsets, row_index, total_m, a_rows, N, K, a, b, y, stream);
+    case kRows16x32:
+      return grouped_cfg<16, 32, 2, 8, GATHER, WIDE>(G, m_offsets, row_index, total_m, a_rows, N, K, a, b, y, stream);
+    default:
+      return grouped_cfg<32, 32, 2, 8, GATHER, WIDE>(G, m_offsets, row_index, total_m, a_rows, N, K, a, b, y, stream);
+  }
+}
+
 }  // namespace
+
+bool fp8_grouped_streams(int64_t G, int64_t total_m, int64_t N, int64_t K) {
+  return grouped_outputs(G, total_m, N, K) != kTiles;
+}
+
+hipError_t launch_fp8_grouped_stream(int32_t G, const int32_t* m_offsets, const int32_t* row_index,
+                                     int64_t total_m, int64_t a_rows, int64_t N, int64_t K,
+                                     Fp8Operand a, Fp8Operand b, Fp8Out y, hipStream_t stream) {
+  auto go = [&](auto wide) {
+    constexpr bool W = decltype(wide)::value;
+    return row_index != nullptr
+               ? grouped_rows<true, W>(G, m_offsets, row_index, total_m, a_rows, N, K, a, b, y, stream)
+               : grouped_rows<false, W>(G, m_offsets, row_index, total_m, a_rows, N, K, a, b, y, stream);
+  };
+  return y.dtype == 0 ? go(std::true_type{}) : go(std::false_type{});
+}
 
 bool fp8_streams(int64_t M, int64_t N) { return M <= 16 || outputs<32, 32>(M, N) <= kCUs; }
 

@@ -150,6 +150,10 @@ bool fp8_streams(int64_t M, int64_t N);
 hipError_t launch_fp8_stream(int64_t M, int64_t N, int64_t K, Fp8Operand a, Fp8Operand b,
                              int b_block_rows, Fp8Out y, hipStream_t stream);
 // row_index != nullptr: a_rows * K < 2^31
+bool fp8_grouped_streams(int64_t G, int64_t total_m, int64_t N, int64_t K);
+hipError_t launch_fp8_grouped_stream(int32_t G, const int32_t* m_offsets, const int32_t* row_index,
+                                     int64_t total_m, int64_t a_rows, int64_t N, int64_t K,
+                                     Fp8Operand a, Fp8Operand b, Fp8Out y, hipStream_t stream);
 hipError_t launch_fp8_grouped(int32_t G, const int32_t* m_offsets, const int32_t* row_index,
                               int64_t total_m, int64_t a_rows, int64_t N, int64_t K, Fp8Operand a,
                               Fp8Operand b, Fp8Out y, hipStream_t stream);

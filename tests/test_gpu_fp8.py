@@ -274,7 +274,8 @@ def test_gemm_past_4_gib():
     close(y[rows], (np_(q[rows]), np_(s[:, rows])), b, 128, "bf16")
 
 
-GROUPS = [[5], [0, 3, 0, 40, 1], [16] * 9, [130, 0, 257, 64, 1], [1, 2] * 40, [0, 0, 700], [33, 64, 65, 0]]
+GROUPS = [[5], [0, 3, 0, 40, 1], [16] * 9, [130, 0, 257, 64, 1], [1, 2] * 40, [0, 0, 700], [33, 64, 65, 0],
+          [0] * 70 + [5] + [0] * 80 + [20], [1] * 130]
 
 
 @pytest.mark.parametrize("counts", GROUPS, ids=lambda c: f"G{len(c)}t{sum(c)}")
@@ -302,15 +303,16 @@ def test_grouped(counts, N, K, gather, out):
         close(torch.from_numpy(y[lo:hi]), (q, s), (b[0][e], b[1][e]), 128, out)
 
 
-@pytest.mark.parametrize("counts", [[0, 400, 3, 130, 128, 250, 289, 100],
-                                    [0, 1000, 300, 257, 1, 511, 700, 256, 900, 640, 5, 833, 720, 610, 512, 900]],
-                         ids=lambda c: f"G{len(c)}t{sum(c)}")
+@pytest.mark.parametrize("counts,N,K", [
+    ([20, 0, 64, 65, 1] * 9, 2056, 144), ([20, 0, 64, 65, 1] * 18, 1032, 1040), ([0, 400, 3, 130, 128, 250, 289, 100], 4104, 144),
+    ([0, 1000, 300, 257, 1, 511, 700, 256, 900, 640, 5, 833, 720, 610, 512, 900], 4104, 144),
+    ([1, 0, 3, 9, 2, 17, 0, 33], 1032, 1040), ([1, 0, 2, 1, 3], 2056, 1040), ([40, 3, 0, 33, 70], 520, 2064)],
+    ids=lambda c: f"G{len(c)}t{sum(c)}" if isinstance(c, list) else str(c))
 @pytest.mark.parametrize("gather", [False, True])
 @pytest.mark.parametrize("out", ["f32", "bf16"])
-def test_grouped_many_tiles(counts, gather, out):
-    """Rows enough for the larger tiles, which few columns never take; each
-    expert's edge rows and some more."""
-    N, K = 4104, 144
+def test_grouped_many_tiles(counts, N, K, gather, out):
+    """Rows and columns for every tile shape; each expert's edge rows and some
+    more."""
     rng = np.random.default_rng(sum(counts))
     off = wl.ragged_offsets(counts)
     total, G = int(off[-1]), len(counts)
