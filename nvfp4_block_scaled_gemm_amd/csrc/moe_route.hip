@@ -9,7 +9,8 @@
 // with n the tokens that chose any expert (a token is masked, or an expert
 // is at -inf, and then never chosen).
 //
-// Forward, two launches (one token costs one pass over its logits):
+// Forward, two launches, or one for few tokens (a token costs one pass over
+// its logits):
 //  1. route_choose_kernel: LPT lanes hold a token's logits in registers, NPL
 //     neighbouring experts each.  A logit and its expert make one 31-bit key
 //     (the order-keeping image of the logit, cut to leave room for the
@@ -28,6 +29,12 @@
 //     one more per 64 experts sums their share of the loss.
 // Backward, one launch: the softmax again from the logits (one read, one
 // write); the chosen weights' gradients meet their experts through LDS.
+//
+// The choice is bound by the vector unit (1.5 k instructions a logit besides
+// the softmax's), the rest by launches and latency.  Measured,
+// bf16, 256 experts, top 8: 1 token 6.3 us forward and 3.3 backward, 4096
+// tokens 16.2 and 4.2, 65536 40.7 (34 MB of logits; of it the choice 28) and
+// 17.2 (67 MB, 3.9 TB/s).
 #include "nvfp4_device.h"
 #include "nvfp4_internal.h"
 
@@ -206,8 +213,9 @@ __host__ inline Partials partials_at(void* ws, int64_t chunks, int64_t E) {
 }
 
 // Choices are walked as (token, slot) pairs of kMaxTop slots a token, so no
-// index is divided by k.
-template <int LPT, int NPL, int DT, bool VEC>
+// index is divided by k.  ONE: at most kSub tokens, and the workgroup finishes
+// the call by itself.
+template <int LPT, int NPL, int DT, bool VEC, bool ONE>
 __global__ __launch_bounds__(1024) void route_choose_kernel(
     int T, int E, int k, const void* __restrict__ x, int64_t ld, const uint8_t* __restrict__ mask, bool renorm, int per_chunk, RouteOut out, Partials part) {
   constexpr int TPW = 64 / LPT;  // tokens of a wave
@@ -227,16 +235,40 @@ __global__ __launch_bounds__(1024) void route_choose_kernel(
   }
   if (tid == 0) {
     routed = 0;
-    if (blockIdx.x == 0) *part.written = 0;
+    if (!ONE && blockIdx.x == 0) *part.written = 0;
   }
+  if constexpr (ONE) {
+    for (int i = tid; i < EP * kSubWords; i += blockDim.x) (&bits[0][0])[i] = 0;
+    __syncthreads();
+  }
+  // place of token tk of the 256 among the expert's tokens
+  auto place_of = [&](int e, int tk) {
+    if (e < 0) return -1;
+    int32_t place = before[e];
+#pragma unroll
+    for (int w = 0; w < kSubWords; ++w) {
+      const uint32_t b = bits[e][w];
+      const int d = tk - 32 * w;
+      place += __builtin_popcount(d >= 32 ? b : (d > 0 ? b & ((1u << d) - 1u) : 0u));
+    }
+    return place;
+  };
+  auto chosen_by = [&](int e) {
+    int32_t n = 0;
+#pragma unroll
+    for (int w = 0; w < kSubWords; ++w) n += __builtin_popcount(bits[e][w]);
+    return n;
+  };
   float ps[NPL];
 #pragma unroll
   for (int i = 0; i < NPL; ++i) ps[i] = 0.f;
   int mine = 0;  // tokens routed, counted by lane 0 of each group
   for (int s0 = c0; s0 < c1; s0 += kSub) {
     const int here = min(kSub, c1 - s0);
-    for (int i = tid; i < EP * kSubWords; i += blockDim.x) (&bits[0][0])[i] = 0;
-    __syncthreads();
+    if constexpr (!ONE) {
+      for (int i = tid; i < EP * kSubWords; i += blockDim.x) (&bits[0][0])[i] = 0;
+      __syncthreads();
+    }
     // one turn ahead of itself: a turn loads the next tokens' logits and then
     // works on its own (the first only loads)
     float nv[NPL];
@@ -289,30 +321,15 @@ __global__ __launch_bounds__(1024) void route_choose_kernel(
       if (lg == 0 && active) ++mine;
     }
     __syncthreads();
+    if constexpr (ONE) break;
     // places within the chunk, by token
     for (int i = tid; i < here * kMaxTop; i += blockDim.x) {
       const int tk = i / kMaxTop, j = i % kMaxTop;
       if (j >= k) continue;
-      const int e = chosen[tk][j];
-      int32_t place = -1;
-      if (e >= 0) {
-        place = before[e];
-#pragma unroll
-        for (int w = 0; w < kSubWords; ++w) {
-          const uint32_t b = bits[e][w];
-          const int d = tk - 32 * w;
-          place += __builtin_popcount(d >= 32 ? b : (d > 0 ? b & ((1u << d) - 1u) : 0u));
-        }
-      }
-      out.pair_row[(int64_t)(s0 + tk) * k + j] = place;
+      out.pair_row[(int64_t)(s0 + tk) * k + j] = place_of(chosen[tk][j], tk);
     }
     __syncthreads();
-    for (int e = tid; e < E; e += blockDim.x) {
-      int32_t n = 0;
-#pragma unroll
-      for (int w = 0; w < kSubWords; ++w) n += __builtin_popcount(bits[e][w]);
-      before[e] += n;
-    }
+    for (int e = tid; e < E; e += blockDim.x) before[e] += chosen_by(e);
     __syncthreads();
   }
   // probability sums: the wave's groups, then every fourth wave in order
@@ -329,9 +346,59 @@ __global__ __launch_bounds__(1024) void route_choose_kernel(
     }
     __syncthreads();
   }
+  auto mass = [&](int e) { return (psum[0][e] + psum[1][e]) + (psum[2][e] + psum[3][e]); };
+  if constexpr (ONE) {
+    __shared__ int32_t wave_sum[16];
+    __shared__ double wave_loss[16];
+    int32_t end = 0;  // rows of the experts so far
+    double loss = 0.0;
+    for (int b = 0; b < E; b += blockDim.x) {
+      const int e = b + tid;
+      const int32_t n = e < E ? chosen_by(e) : 0;
+      int32_t v = n;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int32_t o = __shfl_up(v, d, 64);
+        if (lane >= d) v += o;
+      }
+      if (lane == 63) wave_sum[wave] = v;
+      __syncthreads();
+      v += end;
+      for (int w = 0; w < waves; ++w) {
+        if (w < wave) v += wave_sum[w];
+        end += wave_sum[w];
+      }
+      if (e < E) {
+        before[e] = v - n;
+        out.counts[e] = n;
+        out.m_offsets[e + 1] = v;
+        loss += (double)n * (double)mass(e);
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) loss += __shfl_xor(loss, d, 64);
+    if (lane == 0) wave_loss[wave] = loss;
+    for (int i = tid; i < T * kMaxTop; i += blockDim.x) {
+      const int t = i / kMaxTop, j = i % kMaxTop;
+      if (j >= k) continue;
+      const int32_t place = place_of(chosen[t][j], t);
+      out.pair_row[t * k + j] = place;
+      if (place >= 0) out.row_index[place] = t;
+    }
+    for (int i = end + tid; i < T * k; i += blockDim.x) out.row_index[i] = -1;
+    __syncthreads();
+    if (tid != 0) return;
+    loss = 0.0;
+    for (int w = 0; w < waves; ++w) loss += wave_loss[w];
+    out.m_offsets[0] = 0;
+    out.routed[0] = routed;
+    out.loss[0] = routed > 0 ? (float)((double)E * loss / ((double)routed * (double)routed * k)) : 0.f;
+    return;
+  }
   for (int e = tid; e < E; e += blockDim.x) {
     part.counts[(int64_t)blockIdx.x * E + e] = before[e];
-    part.psum[(int64_t)blockIdx.x * E + e] = (psum[0][e] + psum[1][e]) + (psum[2][e] + psum[3][e]);
+    part.psum[(int64_t)blockIdx.x * E + e] = mass(e);
   }
   if (tid == 0) part.routed[blockIdx.x] = routed;
 }
@@ -633,8 +700,13 @@ size_t moe_route_workspace_bytes(int64_t T, int64_t E) {
 hipError_t launch_moe_route(int64_t T, int64_t E, int topk, const void* logits, int dtype,
                             int64_t ld, const uint8_t* mask, bool renorm, RouteOut out,
                             void* workspace, hipStream_t stream) {
-  const int64_t per = chunk_tokens(T);
-  const int chunks = T > 0 ? (int)((T + per - 1) / per) : 1;  // no token: one empty chunk
+  // One workgroup takes the whole call where it needs about one turn for it
+  // (bf16, us, one launch and two: 1 x 256 top 8 6.3 / 9.4, 16 x 256 6.5 / 10.1,
+  // 64 x 128 8.5 / 9.4, 16 x 1024 top 16 13.0 / 17.7, 64 x 256 10.9 / 10.2, but
+  // 128 x 128 11.9 / 9.1, 64 x 512 top 10 16.1 / 12.2).
+  const bool one = T <= 64 && T * E <= 16384;
+  const int64_t per = one ? T : chunk_tokens(T);
+  const int chunks = one ? 1 : (int)((T + per - 1) / per);
   const Partials part = partials_at(workspace, chunks, E);
   const hipError_t err = by_experts(E, [&](auto lpt, auto npl) {
     constexpr int LPT = decltype(lpt)::value, NPL = decltype(npl)::value;
@@ -642,13 +714,17 @@ hipError_t launch_moe_route(int64_t T, int64_t E, int topk, const void* logits, 
     int64_t waves = (per * LPT + 63) / 64;
     waves = waves > 16 ? 16 : (waves < 4 ? 4 : waves);
     return by_rows(dtype, rows_vec(logits, dtype, ld, E, NPL), [&](auto dt, auto vec) {
-      route_choose_kernel<LPT, NPL, decltype(dt)::value, decltype(vec)::value>
-          <<<(unsigned)chunks, (unsigned)(64 * waves), 0, stream>>>(
-              (int)T, (int)E, topk, logits, ld, mask, renorm, (int)per, out, part);
+      auto choose = [&](auto whole_call) {
+        route_choose_kernel<LPT, NPL, decltype(dt)::value, decltype(vec)::value, decltype(whole_call)::value>
+            <<<(unsigned)chunks, (unsigned)(64 * waves), 0, stream>>>(
+                (int)T, (int)E, topk, logits, ld, mask, renorm, (int)per, out, part);
+      };
+      if (one) choose(std::true_type{});
+      else choose(std::false_type{});
       return hipGetLastError();
     });
   });
-  if (err != hipSuccess) return err;
+  if (err != hipSuccess || one) return err;
   const int loss_parts = (int)((E + 63) / 64);
   route_place_kernel<<<(unsigned)(chunks + loss_parts), 1024, 0, stream>>>(
       (int)T, (int)E, topk, chunks, (int)per, loss_parts, out, part);
@@ -665,7 +741,9 @@ hipError_t launch_moe_route_backward(int64_t T, int64_t E, int topk, const void*
     constexpr int LPT = decltype(lpt)::value, NPL = decltype(npl)::value;
     const int64_t groups = 256 / LPT;
     int64_t grid = (T + groups - 1) / groups;
-    if (grid > 1024) grid = 1024;  // four workgroups a CU, several tokens each
+    // four workgroups a CU, several tokens each (65536 x 256: 512 workgroups 22.1
+    // us, 1024 17.3, 2048 18.6, 4096 20.6)
+    if (grid > 1024) grid = 1024;
     const bool whole = rows_vec(logits, dtype, ld, E, NPL) && rows_vec(d_logits, dtype, ld_d, E, NPL);
     return by_rows(dtype, whole, [&](auto dt, auto vec) {
       route_backward_kernel<LPT, NPL, decltype(dt)::value, decltype(vec)::value>

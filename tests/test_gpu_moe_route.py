@@ -39,7 +39,8 @@ def check(x, k, mask=None, renorm=False, route=None):
 
 
 CASES = [(1, 8, 2), (1, 1, 1), (3, 64, 6), (16, 128, 8), (17, 7, 7), (64, 256, 8), (300, 60, 4), (257, 100, 3),
-         (40, 257, 5), (33, 512, 16), (50, 1024, 9), (20, 1000, 8), (1000, 16, 2), (5000, 72, 2)]
+         (40, 257, 5), (33, 512, 16), (50, 1024, 9), (20, 1000, 8), (1000, 16, 2), (5000, 72, 2),
+         (64, 200, 8), (65, 200, 8), (16, 1024, 16), (33, 8, 8), (100, 256, 8), (0, 40, 3)]
 
 
 @pytest.mark.parametrize("T,E,k", CASES)
