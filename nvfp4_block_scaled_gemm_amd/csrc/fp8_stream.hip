@@ -349,6 +349,12 @@ hipError_t launch_fp8_grouped_stream(int32_t G, const int32_t* m_offsets, const 
   return y.dtype == 0 ? go(std::true_type{}) : go(std::false_type{});
 }
 
+// Up to 16 rows the weights' stream is all that counts (us, here and in tiles:
+// 16 x 4096 x 4096 8.9 / 11.1, 16 x 8192 x 8192 17.2 / 20.2, 16 x 32768 x 2048
+// 17.1 / 20.2); otherwise as long as 32 x 32 outputs give every CU at most one
+// workgroup (64 x 4096 x 4096 11.3 / 13.4, 512 x 512 x 8192 17.7 / 16.9 and
+// with fp32 outputs 19.3 / 25.9; but 32 x 12288 x 4096 19.8 / 14.2, 128 x 4096 x
+// 2048 10.8 / 7.8).
 bool fp8_streams(int64_t M, int64_t N) { return M <= 16 || outputs<32, 32>(M, N) <= kCUs; }
 
 hipError_t launch_fp8_stream(int64_t M, int64_t N, int64_t K, Fp8Operand a, Fp8Operand b,
