@@ -91,6 +91,45 @@ def test_training_step_of_a_mixture_layer():
     assert total == T * k and off[-1] == int(live.sum())
 
 
+@pytest.mark.parametrize("T", [1, 4, 16, 64])
+def test_a_decode_step_captured_and_replayed(T):
+    """Router, quantiser and experts' product of few tokens in a graph, with
+    eager steps between the replays; against eager and against fp64."""
+    need_gpu()
+    E, k, N, K = 32, 4, 272, 1040
+    g = torch.Generator().manual_seed(T)
+    wq = nv.nvfp4_fp8_quantize((torch.randn(E, N, K, generator=g) * K ** -0.5).to(DEV), block_rows=128)
+    xs = [(torch.randn(T, K, generator=g).to(DEV), torch.randn(T, E, generator=g).to(DEV)) for _ in range(4)]
+
+    def decode(x, logits):
+        route = nv.nvfp4_moe_route(logits, k, renormalize=True)
+        xq = nv.nvfp4_fp8_quantize(x)
+        h = nv.nvfp4_fp8_grouped_gemm(route.m_offsets, T * k, xq, wq, "f32", row_index=route.row_index)
+        return (h[route.pair_row.long()] * route.weights[..., None]).sum(1), route, xq
+
+    note(f"fp8 mixture decode step T {T}")
+    eager = [decode(*v) for v in xs]
+    wv = values_of(wq, 128).cpu()
+    for out, route, xq in eager:
+        w = wv[route.expert_index.long().cpu()]                       # [T, k, N, K]
+        h = (w * values_of(xq).cpu()[:, None, None, :]).sum(-1)
+        want = (h * route.weights.double().cpu()[..., None]).sum(1)
+        # fp32 accumulation alone, as above
+        assert float((out.double().cpu() - want).norm()) <= 2e-6 * float(want.norm())
+    xin, lin = xs[0][0].clone(), xs[0][1].clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        replayed, _, _ = decode(xin, lin)
+    for i in (1, 2, 3, 0, 2):
+        xin.copy_(xs[i][0])
+        lin.copy_(xs[i][1])
+        graph.replay()
+        again = decode(*xs[i])[0]
+        torch.cuda.synchronize()
+        assert torch.equal(replayed, eager[i][0]) and torch.equal(again, eager[i][0])
+
+
 def test_the_router_feeds_the_4_bit_experts():
     """nvfp4_grouped_gemm reads the router's order as it stands."""
     need_gpu()
