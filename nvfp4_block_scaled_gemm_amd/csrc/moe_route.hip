@@ -49,9 +49,10 @@ __host__ __device__ inline int64_t chunk_tokens(int64_t T) {
   return c < 16 ? 16 : (c + 15) / 16 * 16;
 }
 
-// Order-keeping map of fp32 to unsigned.
+// Order-keeping map of fp32 to unsigned; zeros of either sign are one value
+// (-0 + 0 is +0, and without that the image of -0 would lie below that of +0).
 __device__ __forceinline__ uint32_t key_of(float x) {
-  const uint32_t b = __float_as_uint(x);
+  const uint32_t b = __float_as_uint(x + 0.0f);
   return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 // The image of -inf: what is not above it is never chosen.

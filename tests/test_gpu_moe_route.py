@@ -63,6 +63,19 @@ def test_ties_go_to_the_lowest_expert(E):
     check(x.bfloat16(), 5, renorm=True)
 
 
+@pytest.mark.parametrize("T,E,k", [(12, 8, 1), (64, 40, 5), (70, 256, 8), (40, 1024, 16), (300, 512, 3)])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_zeros_of_either_sign_are_equal(T, E, k, dtype):
+    """Rows of -1, -0 and +0 with fewer ones than choices, so that the border of
+    the choice lies among zeros: the lowest experts of them, whatever their sign."""
+    g = torch.Generator().manual_seed(T + E)
+    x = torch.tensor([-1.0, -0.0, 0.0])[torch.randint(0, 3, (T, E), generator=g)]
+    x[1::2, E // 2] = 1.0
+    x[0, :3] = torch.tensor([-0.0, 0.0, -1.0])
+    note(f"route zeros of either sign {T}x{E} top {k} {dtype}")
+    check(x.bfloat16() if dtype == "bf16" else x, k)
+
+
 @pytest.mark.parametrize("renorm", [False, True])
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_closed_experts_and_empty_rows(renorm, dtype):
