@@ -85,6 +85,19 @@ __device__ __forceinline__ float group_sum(float v) {
   return group_reduce<LPT>(v, [](float a, float b) { return a + b; });
 }
 
+// exp(d), d <= 0, within 2^-22 relative however far d is.  The instruction
+// raises 2 to t = d log2(e), whose rounding alone is up to 2^-24 |t| (5e-6 of
+// the result at d = -88): what t loses is kept in r and put back as
+// 2^t (1 + r ln 2).  Zero from d = -200 on, where -inf would have no r.
+__device__ __forceinline__ float exp_below(float d) {
+  constexpr float kLog2e = 1.44269502f, kLog2eRest = 1.92596303e-8f, kLn2 = 0.693147181f;
+  d = fmaxf(d, -200.0f);
+  const float t = d * kLog2e;
+  const float r = __builtin_fmaf(d, kLog2eRest, __builtin_fmaf(d, kLog2e, -t));
+  const float y = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(y, r * kLn2, y);
+}
+
 // A logit as fp32.
 template <int DT>
 __device__ __forceinline__ float logit(const void* __restrict__ x, int64_t at) {
@@ -298,7 +311,11 @@ __global__ __launch_bounds__(1024) void route_choose_kernel(
 #pragma unroll
       for (int i = 1; i < NPL; ++i) top = fmaxf(top, v[i]);
       top = group_reduce<LPT>(top, [](float p, float q) { return fmaxf(p, q); });
-      // softmax over all, and over the chosen (lane j holds the j-th)
+      // softmax over all, and over the chosen (lane j holds the j-th).  The
+      // sum's terms may take the plain instruction, whose error grows with a
+      // term's distance d from the top: it adds up to 2^-24 times the mean
+      // distance under p, which is at most ln E.  (exp_below here: 40.3 instead
+      // of 38.0 us for 65536 x 256 bf16.)
       const bool active = top > -__builtin_inff();
       if (!active) top = 0.f;
       float sum = 0.f;
@@ -311,7 +328,7 @@ __global__ __launch_bounds__(1024) void route_choose_kernel(
       const float inv = active ? 1.0f / sum : 0.f;
 #pragma unroll
       for (int i = 0; i < NPL; ++i) ps[i] += v[i] * inv;
-      const float ez = got >= 0 ? __expf(val - top) : 0.f;
+      const float ez = got >= 0 ? exp_below(val - top) : 0.f;
       const float chosen_sum = group_sum<LPT>(ez);
       if (tk < here && lg < k) {
         chosen[tk][lg] = (int16_t)got;
@@ -603,7 +620,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(
     float sum = 0.f, dot = 0.f;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
-      v[i] = __expf(v[i] - top);  // an inactive row's -inf gives 0
+      v[i] = exp_below(v[i] - top);  // an inactive row's -inf gives 0
       sum += v[i];
     }
     sum = group_sum<LPT>(sum);
@@ -621,7 +638,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(
       if (e < 0 || e >= E) e = -1;
       if (e >= 0) {
         dw = d_weights[t * k + lg];
-        ez = __expf(logit<DT>(x, t * ld + e) - top);
+        ez = exp_below(logit<DT>(x, t * ld + e) - top);
       }
     }
     float a;

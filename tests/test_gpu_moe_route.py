@@ -97,6 +97,36 @@ def test_closed_experts_and_empty_rows(renorm, dtype):
     back(x, 6, r, ref, mask, renorm)
 
 
+@pytest.mark.parametrize("T,E,k", [(9, 8, 8), (80, 40, 16), (70, 300, 4)])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_far_logits_keep_fp32_weights_and_gradients(T, E, k, dtype, renorm):
+    """Every logit but one lies 20 to 80 below the top, in steps of 1/2, so the
+    distances are exact.  Counted in 2^-24 relative: exp 3 (two of the
+    instruction, one of its correction), the reciprocal and the product 2, one
+    more for second-order terms; the sum is 1 and rounds away at most
+    E exp(-20) = E * 0.035.  A gradient of an expert that was not chosen is
+    -p <p, dw> with positive dw: the same error twice."""
+    g = torch.Generator().manual_seed(E)
+    x = -0.5 * torch.randint(40, 161, (T, E), generator=g).float()
+    x[torch.arange(T), torch.randint(0, E, (T,), generator=g)] = 0.0
+    x = x.bfloat16() if dtype == "bf16" else x
+    note(f"route far logits {T}x{E} top {k} {dtype} renorm {renorm}")
+    r = nv.nvfp4_moe_route(x.to(DEV), k, renormalize=renorm)
+    ref = moe_route_ref(x.float().numpy(), k, None, renorm)
+    assert np.array_equal(np_(r.expert_index), ref["expert_index"])
+    rel = (6 + 0.035 * E) * 2.0 ** -24
+    assert np.abs(np_(r.weights) / ref["weights"] - 1).max() <= rel
+    if dtype == "bf16" or renorm or E == k:
+        return
+    dw = torch.rand(T, k, generator=g) + 0.5
+    got = np_(nv.nvfp4_moe_route_backward(x.to(DEV), r, dw.to(DEV)))
+    want = moe_route_backward_ref(ref, k, dw.numpy(), 0.0)
+    rest = np.ones((T, E), bool)
+    np.put_along_axis(rest, ref["expert_index"], False, 1)
+    assert np.abs(got[rest] / want[rest] - 1).max() <= 2 * rel
+
+
 def test_all_masked_and_no_tokens():
     note("route with no token")
     for x, mask in ((logits_of(9, 12, 1, "fp32"), torch.zeros(9, dtype=torch.bool)),
