@@ -908,26 +908,26 @@ def nvfp4_moe_route(logits: torch.Tensor, topk: int, mask: torch.Tensor | None =
 
 def _moe_route(logits, topk: int, mask, renormalize: bool, workspace, T: int, E: int, ld: int,
                dev: int) -> MoeRoute:
-    n = T * topk
-    need = nvfp4_moe_route_workspace_bytes(T, E) if workspace is None else 0
-    # one allocation for the outputs; its tail is the workspace
-    buf = logits.new_empty(4 * n + 2 * E + 3 + -(-need // 4), dtype=torch.int32)
-    ei, w, ri, pr, counts, off, routed, loss, _ = buf.split_with_sizes(
-        (n, n, n, n, E, E + 1, 1, 1, -(-need // 4)))
-    p = buf.data_ptr()
-    at = p + 16 * n               # counts, m_offsets, routed, loss, workspace
-    ws, ws_bytes = at + 8 * E + 12, need
-    if workspace is not None:
-        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    # every output is an allocation of its own: writing one in place leaves the
+    # others' versions alone (a backward may have saved them), and keeping one
+    # keeps no other
+    like = torch.empty_like
+    ei = logits.new_empty((T, topk), dtype=torch.int32)
+    new, routed = ei.new_empty, ei.new_empty(1)
+    r = MoeRoute(ei, like(ei, dtype=torch.float32), new(E), new(E + 1), new(T * topk), like(ei), routed,
+                 like(routed, dtype=torch.float32))
+    if workspace is None:
+        ws_bytes = nvfp4_moe_route_workspace_bytes(T, E)
+        workspace = new(-(-ws_bytes // 4))
+    else:
+        ws_bytes = workspace.numel() * workspace.element_size()
     st = nvfp4_moe_route_raw(T, E, topk, logits.data_ptr(), _DT_IN[logits.dtype], ld,
                              None if mask is None else mask.data_ptr(),
-                             NVFP4_ROUTE_RENORMALIZE if renormalize else 0, p, p + 4 * n, at,
-                             at + 4 * E, p + 8 * n, p + 12 * n, at + 8 * E + 4, at + 8 * E + 8, ws,
-                             ws_bytes, _stream(None, dev))
+                             NVFP4_ROUTE_RENORMALIZE if renormalize else 0, *[t.data_ptr() for t in r],
+                             workspace.data_ptr(), ws_bytes, _stream(None, dev))
     if st != NVFP4_OK:
         _check("nvfp4_moe_route", st)
-    return MoeRoute(ei.view(T, topk), w.view(torch.float32).view(T, topk), counts, off, ri,
-                    pr.view(T, topk), routed, loss.view(torch.float32))
+    return r
 
 
 def nvfp4_moe_route_backward(logits: torch.Tensor, route: MoeRoute,

@@ -252,6 +252,47 @@ def test_strided_logits_workspace_and_out():
     assert bool((out[:, :5] == 9.0).all()) and bool((out[:, 69:] == 9.0).all())
 
 
+@pytest.mark.parametrize("T", [0, 9, 700])
+def test_outputs_are_tensors_of_their_own(T):
+    """Scaling the weights in place leaves what a backward saved as it was,
+    and keeping the loss keeps nothing else alive."""
+    x = logits_of(T, 16, 3, "fp32").to(DEV)
+    note(f"route outputs T {T}")
+    r = nv.nvfp4_moe_route(x, 4)
+    held = [t.untyped_storage().data_ptr() for t in r if t.numel()]
+    assert len(set(held)) == len(held)
+    before = {n: t._version for n, t in r._asdict().items()}
+    r.weights.mul_(2.0)
+    assert {n for n, t in r._asdict().items() if t._version != before[n]} == {"weights"}
+    assert r.loss.untyped_storage().nbytes() == 4
+
+
+class _Route(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, k):
+        r = nv.nvfp4_moe_route(x, k)
+        ctx.save_for_backward(x, r.expert_index, r.counts, r.routed)
+        ctx.mark_non_differentiable(r.expert_index)
+        return r.weights, r.expert_index
+
+    @staticmethod
+    def backward(ctx, d_weights, _):
+        x, index, counts, routed = ctx.saved_tensors
+        r = nv.MoeRoute(index, None, counts, None, None, None, routed, None)
+        return nv.nvfp4_moe_route_backward(x, r, d_weights.contiguous()), None
+
+
+def test_weights_scaled_in_place_before_the_backward():
+    x = logits_of(30, 16, 4, "fp32").to(DEV)
+    dw = torch.randn(30, 4, generator=torch.Generator().manual_seed(1)).to(DEV)
+    note("route weights scaled in place")
+    z = x.clone().requires_grad_(True)
+    w, _ = _Route.apply(z, 4)
+    w.mul_(2.0)
+    w.backward(dw)
+    assert torch.equal(z.grad, nv.nvfp4_moe_route_backward(x, nv.nvfp4_moe_route(x, 4), 2 * dw))
+
+
 def test_captured_and_replayed():
     """Two graphs with their own outputs and workspaces, replayed beside eager
     calls with changing logits."""
