@@ -261,6 +261,10 @@ hipError_t stream_cfg(int64_t M, int64_t N, int64_t K, Fp8Operand a, Fp8Operand 
   return hipGetLastError();
 }
 
+// WIDE: how 32-row tiles multiply.  16-row tiles always take the 16-bit
+// instructions and their fp32 sums, bf16 outputs too: the loads hide them (us,
+// 8-bit and wide: 1 x 8192 x 8192 14.6 / 14.6, 16 x 4096 x 4096 7.6 / 7.5, 32 x
+// 4096 x 4096 8.9 / 9.2; of 32-row tiles 64 x 4096 x 4096 10.9 / 14.3).
 template <bool BROWS, bool WIDE>
 hipError_t stream_rows(int64_t M, int64_t N, int64_t K, Fp8Operand a, Fp8Operand b, Fp8Out y,
                        hipStream_t stream) {
@@ -276,10 +280,10 @@ hipError_t stream_rows(int64_t M, int64_t N, int64_t K, Fp8Operand a, Fp8Operand
   // each still has two blocks (M = 1, 4096 x 4096 7.7 -> 7.0 us, M = 16
   // 7.7 -> 8.2; 2560 x 2048 4.1 -> 4.3).
   if (M <= 4 && K >= 32 * kBlock)
-    return stream_cfg<16, 16, 2, 16, BROWS, WIDE>(M, N, K, a, b, y, stream);
-  if (M <= 8 || one16) return stream_cfg<16, 16, 4, 8, BROWS, WIDE>(M, N, K, a, b, y, stream);
+    return stream_cfg<16, 16, 2, 16, BROWS, true>(M, N, K, a, b, y, stream);
+  if (M <= 8 || one16) return stream_cfg<16, 16, 4, 8, BROWS, true>(M, N, K, a, b, y, stream);
   if (M <= 16 || outputs<16, 32>(M, N) <= kCUs)
-    return stream_cfg<16, 32, 2, 8, BROWS, WIDE>(M, N, K, a, b, y, stream);
+    return stream_cfg<16, 32, 2, 8, BROWS, true>(M, N, K, a, b, y, stream);
   return stream_cfg<32, 32, 2, 8, BROWS, WIDE>(M, N, K, a, b, y, stream);
 }
 
@@ -323,9 +327,9 @@ hipError_t grouped_rows(int32_t G, const int32_t* m_offsets, const int32_t* row_
                         Fp8Operand b, Fp8Out y, hipStream_t stream) {
   switch (grouped_outputs(G, total_m, N, K)) {
     case kRows16x16:
-      return grouped_cfg<16, 16, 4, 8, GATHER, WIDE>(G, m_offsets, row_index, total_m, a_rows, N, K, a, b, y, stream);
+      return grouped_cfg<16, 16, 4, 8, GATHER, true>(G, m_offsets, row_index, total_m, a_rows, N, K, a, b, y, stream);
     case kRows16x32:
-      return grouped_cfg<16, 32, 2, 8, GATHER, WIDE>(G, m_offsets, row_index, total_m, a_rows, N, K, a, b, y, stream);
+      return grouped_cfg<16, 32, 2, 8, GATHER, true>(G, m_offsets, row_index, total_m, a_rows, N, K, a, b, y, stream);
     default:
       return grouped_cfg<32, 32, 2, 8, GATHER, WIDE>(G, m_offsets, row_index, total_m, a_rows, N, K, a, b, y, stream);
   }

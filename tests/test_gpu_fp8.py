@@ -245,6 +245,53 @@ def test_gemm_exact_codes_and_nan_scales(M):
     assert np.isfinite(np.delete(y, 1, 0)[:, :128]).all()
 
 
+def outliers(rng, rows, K, second):
+    """Values of 0.5 to 1.5 and in each block of 128 two of 448, the second as
+    the code given."""
+    q = rng.choice(np.array([0x30, 0x34, 0x38, 0x3C, 0xB0, 0xB8], np.uint8), (rows, K))
+    q[:, 3::128], q[:, 9::128] = 0x7E, second
+    return q, np.exp2(rng.uniform(-2, 2, (-(-K // 128), rows))).astype(np.float32)
+
+
+def few_rows_close(y, a, b, block_rows, out):
+    """Few rows keep fp32 sums for bf16 outputs too: one rounding more."""
+    ref, base = fp8_gemm_ref(*a, *b, block_rows)
+    tol = fp8_tolerance(ref, base, fp8_dequantize_ref(*a), fp8_dequantize_ref(*b, block_rows), "f32")
+    if out == "bf16":
+        tol = tol + 2.0 ** -8 * (np.abs(ref) + tol)
+    bad = np.argwhere(~(np.abs(np_(y).astype(np.float64) - ref) <= tol))
+    assert bad.size == 0, (bad[:4].tolist(), np_(y)[tuple(bad[0])], ref[tuple(bad[0])], tol[tuple(bad[0])])
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 300, 4112), (3, 128, 256), (5, 8200, 400), (16, 520, 2064), (20, 130, 400),
+                                   (30, 4000, 272)])
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_few_rows_with_outliers_that_cancel(M, N, K, block_rows, out):
+    """The two largest products of every block cancel; what is left is a few
+    thousandths of them."""
+    rng = np.random.default_rng(M + N)
+    a, b = outliers(rng, M, K, 0x7E), outliers(rng, N, K, 0xFE)
+    b = b if block_rows == 1 else (b[0], np.ascontiguousarray(b[1][:, ::128]))
+    note(f"fp8 gemm cancelling outliers {M}x{N}x{K} block_rows {block_rows} {out}")
+    few_rows_close(nv.nvfp4_fp8_gemm(to_gpu(a), to_gpu(b), out), a, b, block_rows, out)
+
+
+@pytest.mark.parametrize("counts,N,K", [([2, 0, 1, 3], 300, 4112), ([1, 0, 3, 9, 2, 17, 0, 33], 1032, 1040),
+                                        ([1, 0, 2, 1, 3], 2056, 1040)])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_few_grouped_rows_with_outliers_that_cancel(counts, N, K, out):
+    rng = np.random.default_rng(N)
+    off = wl.ragged_offsets(counts)
+    a, bs = outliers(rng, int(off[-1]), K, 0x7E), [outliers(rng, N, K, 0xFE) for _ in counts]
+    b = (np.stack([q for q, _ in bs]), np.stack([s[:, ::128] for _, s in bs]))
+    note(f"fp8 grouped cancelling outliers {counts} N {N} K {K} {out}")
+    y = nv.nvfp4_fp8_grouped_gemm(off.to(DEV), int(off[-1]), to_gpu(a), to_gpu(b), out)
+    for e, (lo, hi) in enumerate(zip(off[:-1].tolist(), off[1:].tolist())):
+        if lo < hi:
+            few_rows_close(y[lo:hi], (a[0][lo:hi], a[1][:, lo:hi]), (b[0][e], b[1][e]), 128, out)
+
+
 def test_gemm_empty():
     f8 = torch.float8_e4m3fn
     a = (torch.empty(4, 0, dtype=f8, device=DEV), torch.empty(0, 4, device=DEV))
