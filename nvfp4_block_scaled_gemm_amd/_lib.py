@@ -762,7 +762,9 @@ def nvfp4_fp8_gemm(a, b, out_dtype: str = "bf16", y: torch.Tensor | None = None,
                    accumulate: bool = False, stream=None):
     """a = Fp8Packed [M, K] with block_rows 1; b = Fp8Packed [N, K] with
     block_rows 1 or 128 -> y [M, N] = a . b^T.  With accumulate the product
-    is added to the fp32 ``y``.  A linear layer y = x W^T takes x (layout
+    is added to the fp32 ``y``.  out_dtype "f32" keeps fp32 sums throughout;
+    "bf16" may cut each product 2^-16 below the largest of its block
+    (include/nvfp4.h has the bound).  A linear layer y = x W^T takes x (layout
     "rows") and W (block_rows 128, "rows"); its input gradient takes dy
     ("rows") and W ("cols"); its weight gradient dy ("cols") and x ("cols")."""
     a, b = _fp8(a), _fp8(b)

@@ -105,9 +105,12 @@ def fp8_tolerance(y_ref, base, a, b, out_dtype: str):
     scales and of them with the block's sum, and one addition per block, each
     off by at most 2^-24 of a partial sum that sum |A B| bounds.  bf16 outputs
     round once more, by at most 2^-8 of the value, and their blocks are summed
-    by the 8-bit matrix instruction, which aligns products to the largest one:
-    an in-bounds check of the instruction alone gave up to 2^-11.2 of the
-    largest of 128 products, counted here as 2^-10 of max |A| max |B|."""
+    by the 8-bit matrix instruction, which cuts each product 2^-16 below the
+    largest running sum.  For operands without outliers that costs up to
+    2^-11.2 of the largest of 128 products (an in-bounds check of the
+    instruction alone), counted here as 2^-10 of max |A| max |B|.  It is no
+    bound for all operands: that is 2^-9 sum |A B|, and blocks of one outlier
+    and 127 small products come near it."""
     K = a.shape[1]
     tol = (128 + 3 + -(-K // FP8_BLOCK)) * 2.0 ** -24 * base
     if out_dtype == "bf16":

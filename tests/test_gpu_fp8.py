@@ -7,7 +7,7 @@ import torch
 
 import nvfp4_block_scaled_gemm_amd as nv
 import workloads as wl
-from oracle import (fp8_dequantize_ref, fp8_gemm_ref, fp8_grouped_quantize_t_ref, fp8_quantize_ref, fp8_quantize_t_ref,
+from oracle import (E4M3_TABLE, fp8_dequantize_ref, fp8_gemm_ref, fp8_grouped_quantize_t_ref, fp8_quantize_ref, fp8_quantize_t_ref,
                     fp8_tolerance)
 from tests.gpu_util import need_gpu, note, np_
 
@@ -290,6 +290,57 @@ def test_few_grouped_rows_with_outliers_that_cancel(counts, N, K, out):
     for e, (lo, hi) in enumerate(zip(off[:-1].tolist(), off[1:].tolist())):
         if lo < hi:
             few_rows_close(y[lo:hi], (a[0][lo:hi], a[1][:, lo:hi]), (b[0][e], b[1][e]), 128, out)
+
+
+@pytest.mark.parametrize("M,N,K", [(2, 300, 4112), (40, 300, 272), (40, 1500, 272), (300, 1500, 400), (600, 1000, 1040),
+                                   (2048, 8200, 144)])
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("small,large,second", [(None, 0x7E, 0xFE), (0x4F, 0x78, 0xF8), (0x4F, 0x78, 0x4F)])
+def test_gemm_with_outliers(M, N, K, block_rows, out, small, large, second):
+    """Every kernel, with blocks of a few large products that cancel or stand
+    alone and many that lie just above the 8-bit instruction's last bit (7.5 of
+    256^2: half of it is cut): fp32 outputs within fp32 sums, bf16 ones within
+    2^-9 of the sum of magnitudes and their own rounding."""
+    rng = np.random.default_rng(M + K)
+    a, b = outliers(rng, M, K, 0x7E), outliers(rng, N, K, 0xFE)
+    if small is not None:
+        a[0][:], b[0][:] = 0x38, small
+        a[0][:, 3::128] = b[0][:, 3::128] = large
+        a[0][:, 9::128], b[0][:, 9::128] = (large, second) if second > 127 else (0x38, small)
+    b = b if block_rows == 1 else (b[0], np.ascontiguousarray(b[1][:, ::128]))
+    note(f"fp8 gemm outliers {M}x{N}x{K} block_rows {block_rows} {out} {large:#x} {second:#x}")
+    y = nv.nvfp4_fp8_gemm(to_gpu(a), to_gpu(b), out)
+    rows = np.unique(np.concatenate([[0, M - 1], rng.integers(0, M, 24)]))
+    a = (a[0][rows], a[1][:, rows])
+    ref, base = fp8_gemm_ref(*a, *b, block_rows)
+    tol = fp8_tolerance(ref, base, fp8_dequantize_ref(*a), fp8_dequantize_ref(*b, block_rows), "f32")
+    if out == "bf16":
+        tol = tol + 2.0 ** -9 * base
+        tol = tol + 2.0 ** -8 * (np.abs(ref) + tol)
+    got = np_(y[torch.from_numpy(rows).to(DEV)]).astype(np.float64)
+    bad = np.argwhere(~(np.abs(got - ref) <= tol))
+    assert bad.size == 0, (bad[:4].tolist(), got[tuple(bad[0])], ref[tuple(bad[0])], tol[tuple(bad[0])])
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("M,N", [(2, 300), (40, 300), (300, 1500), (1024, 4100)])
+def test_gemm_scales_whose_product_is_tiny(M, N, block_rows):
+    """Scales' products on both sides of 2^-126.  Below it they are rounded to a
+    multiple of 2^-149, off by at most 2^-150 times the block's sum; results
+    below 2^-126 likewise by 2^-150 each of five additions."""
+    rng = np.random.default_rng(M)
+    K = 400
+    a, b = rand_operand(rng, M, K), rand_operand(rng, N, K, block_rows)
+    a = (a[0], (np.exp2(rng.integers(-75, -60, a[1].shape)) * 1.37).astype(np.float32))
+    b = (b[0], (np.exp2(rng.integers(-75, -60, b[1].shape)) * 1.61).astype(np.float32))
+    note(f"fp8 gemm tiny scales {M}x{N} block_rows {block_rows}")
+    y = np_(nv.nvfp4_fp8_gemm(to_gpu(a), to_gpu(b), "f32")).astype(np.float64)
+    ref, base = fp8_gemm_ref(*a, *b, block_rows)
+    va, vb = np.abs(E4M3_TABLE[a[0]]), np.abs(E4M3_TABLE[b[0]])
+    tol = (128 + 3 + 4) * 2.0 ** -24 * base + 2.0 ** -150 * (va @ vb.T) + 5 * 2.0 ** -150
+    bad = np.argwhere(~(np.abs(y - ref) <= tol))
+    assert bad.size == 0, (bad[:4].tolist(), y[tuple(bad[0])], ref[tuple(bad[0])], tol[tuple(bad[0])])
 
 
 def test_gemm_empty():
