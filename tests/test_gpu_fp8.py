@@ -202,6 +202,34 @@ def test_gemm_accumulates(M, N, K, block_rows):
     close(y, a, b, block_rows, "f32", add=y0.astype(np.float64))
 
 
+@pytest.mark.parametrize("M", [1, 3, 4, 5])
+@pytest.mark.parametrize("N,K", [(300, 4096), (4099, 4112), (133, 8208), (72, 4080)])
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("out,add", [("f32", False), ("f32", True), ("bf16", False)])
+def test_gemm_few_rows_of_long_k(M, N, K, block_rows, out, add):
+    """Both sides of the borders (4 rows, K = 4096) of the widest split of K;
+    numbers of blocks that the waves do not share evenly, a last block cut."""
+    rng = np.random.default_rng(M + N + K)
+    a, b = rand_operand(rng, M, K), rand_operand(rng, N, K, block_rows)
+    y0 = rng.standard_normal((M, N)).astype(np.float32) * 1e3 if add else None
+    note(f"fp8 gemm {M}x{N}x{K} block_rows {block_rows} {out} add {add}")
+    y = nv.nvfp4_fp8_gemm(to_gpu(a), to_gpu(b), out, y=torch.from_numpy(y0).to(DEV) if add else None, accumulate=add)
+    close(y, a, b, block_rows, out, add=y0.astype(np.float64) if add else None)
+
+
+@pytest.mark.parametrize("M,N,K,block_rows", [(40, 1500, 272, 128), (500, 500, 272, 1), (600, 1500, 400, 128),
+                                              (1024, 4100, 144, 128), (1024, 4100, 144, 1), (2000, 4100, 144, 128),
+                                              (2000, 4100, 144, 1), (2, 4099, 4112, 128)])
+def test_gemm_accumulates_in_every_shape(M, N, K, block_rows):
+    rng = np.random.default_rng(M + N)
+    a, b = rand_operand(rng, M, K), rand_operand(rng, N, K, block_rows)
+    y0 = rng.standard_normal((M, N)).astype(np.float32) * 1e3
+    y = torch.from_numpy(y0).to(DEV)
+    note(f"fp8 gemm accumulate {M}x{N}x{K} block_rows {block_rows}")
+    nv.nvfp4_fp8_gemm(to_gpu(a), to_gpu(b), "f32", y=y, accumulate=True)
+    close(y, a, b, block_rows, "f32", add=y0.astype(np.float64))
+
+
 @pytest.mark.parametrize("M,N", [(1, 130), (20, 130), (200, 130), (2100, 130)])
 @pytest.mark.parametrize("out,ld,shift", [("bf16", 136, 0), ("bf16", 133, 1), ("f32", 132, 0), ("f32", 131, 3)])
 def test_gemm_writes_only_its_view(M, N, out, ld, shift):
