@@ -299,8 +299,9 @@ int nvfp4_mxfp4_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a_q, const 
  * Errors: NVFP4_ERR_INVALID_ARG for cols % 16 != 0, block_rows not 1 or 128,
  * negative sizes, a bad dtype, ld_x < cols, one pointer of a pair (q, s) or
  * (qt, st) without the other, both pairs null, or a null x;
- * NVFP4_ERR_UNSUPPORTED for x, its rows, q or qt not 16-byte aligned, or a
- * dimension above 2^30.
+ * NVFP4_ERR_UNSUPPORTED for x, its rows, q or qt not 16-byte aligned, a
+ * dimension above 2^30, or sizes whose launch would pass 2^32 threads (here
+ * and in the products below: from about 2^22 blocks or tiles of outputs on).
  */
 int nvfp4_fp8_quantize(const void* x, nvfp4_dtype x_dtype, int64_t batch, int64_t rows,
                        int64_t cols, int64_t ld_x, int block_rows, uint8_t* q, float* s,
@@ -351,8 +352,8 @@ int nvfp4_fp8_grouped_quantize(const void* x, nvfp4_dtype x_dtype, int32_t G,
  * Errors: NVFP4_ERR_INVALID_ARG for K % 16 != 0, b_block_rows not 1 or 128,
  * negative sizes, a bad dtype or flag, NVFP4_ACCUMULATE with a BF16 y,
  * ld_y < N or a null pointer; NVFP4_ERR_UNSUPPORTED for q not 16-byte
- * aligned, s or y not aligned to their elements, K > 2^22 or another
- * dimension above 2^30.
+ * aligned, s or y not aligned to their elements, K > 2^22, another dimension
+ * above 2^30, or sizes whose launch would pass 2^32 threads.
  */
 int nvfp4_fp8_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a_q, const float* a_s,
                    const uint8_t* b_q, const float* b_s, int b_block_rows, void* y,

@@ -108,6 +108,7 @@ int gemm_dispatch(int64_t M, int64_t N, int64_t K, const uint8_t* a_q, const uin
 constexpr int64_t kMaxFp8K = (int64_t)1 << 22;  // 256 rows of K bytes stay below 2^31
 
 bool dtype_ok(int dt) { return dt == NVFP4_F32 || dt == NVFP4_BF16; }
+int from_fp8(hipError_t e) { return e == hipErrorNotSupported ? NVFP4_ERR_UNSUPPORTED : from_hip(e); }
 int64_t dtype_size(int dt) { return dt == NVFP4_F32 ? 4 : 2; }
 
 // Checks both quantisers share; NVFP4_OK, an error, or 1: nothing to do.
@@ -360,7 +361,7 @@ int nvfp4_fp8_quantize(const void* x, nvfp4_dtype x_dtype, int64_t batch, int64_
   if (batch == 0) rows = 0;
   const int v = fp8_quantize_check(x, (int)x_dtype, rows, cols, ld_x, q, s, qt, st);
   if (v != NVFP4_OK) return v == 1 ? NVFP4_OK : v;
-  return from_hip(nvfp4::launch_fp8_quantize(x, (int)x_dtype, batch, rows, cols, ld_x, block_rows,
+  return from_fp8(nvfp4::launch_fp8_quantize(x, (int)x_dtype, batch, rows, cols, ld_x, block_rows,
                                              q, s, qt, st, (hipStream_t)stream));
 }
 
@@ -379,7 +380,7 @@ int nvfp4_fp8_grouped_quantize(const void* x, nvfp4_dtype x_dtype, int32_t G,
   const int v = fp8_quantize_check(x, (int)x_dtype, total_m, cols, ld_x, q, s, qt, st);
   if (v != NVFP4_OK) return v == 1 ? NVFP4_OK : v;
   if (m_offsets == nullptr) return NVFP4_ERR_INVALID_ARG;
-  return from_hip(nvfp4::launch_fp8_grouped_quantize(x, (int)x_dtype, G, m_offsets, row_index,
+  return from_fp8(nvfp4::launch_fp8_grouped_quantize(x, (int)x_dtype, G, m_offsets, row_index,
                                                      total_m, x_rows, cols, ld_x, q, s, qt, st,
                                                      (hipStream_t)stream));
 }
@@ -394,7 +395,7 @@ int nvfp4_fp8_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a_q, const fl
   int v = fp8_out_check(y, (int)y_dtype, N, ld_y, flags);
   if (v == NVFP4_OK && K > 0) v = fp8_operands_check(a_q, a_s, b_q, b_s);
   if (v != NVFP4_OK) return v;
-  return from_hip(nvfp4::launch_fp8_gemm(M, N, K, {a_q, a_s}, {b_q, b_s}, b_block_rows,
+  return from_fp8(nvfp4::launch_fp8_gemm(M, N, K, {a_q, a_s}, {b_q, b_s}, b_block_rows,
                                          fp8_out(y, (int)y_dtype, ld_y, flags),
                                          (hipStream_t)stream));
 }
@@ -415,7 +416,7 @@ int nvfp4_fp8_grouped_gemm(int32_t G, const int32_t* m_offsets, const int32_t* r
   if (v == NVFP4_OK && K > 0) v = fp8_operands_check(a_q, a_s, b_q, b_s);
   if (v != NVFP4_OK) return v;
   if (row_index != nullptr && a_rows * K >= ((int64_t)1 << 31)) return NVFP4_ERR_UNSUPPORTED;
-  return from_hip(nvfp4::launch_fp8_grouped(G, m_offsets, row_index, total_m, a_rows, N, K,
+  return from_fp8(nvfp4::launch_fp8_grouped(G, m_offsets, row_index, total_m, a_rows, N, K,
                                             {a_q, a_s}, {b_q, b_s},
                                             fp8_out(y, (int)y_dtype, ld_y, 0),
                                             (hipStream_t)stream));
@@ -435,7 +436,7 @@ int nvfp4_fp8_grouped_wgrad(int32_t G, const int32_t* m_offsets, int64_t total_m
   int v = fp8_out_check(dw, (int)dw_dtype, K, K, flags);
   if (v == NVFP4_OK && P > 0) v = fp8_operands_check(a_q, a_s, b_q, b_s);
   if (v != NVFP4_OK) return v;
-  return from_hip(nvfp4::launch_fp8_wgrad(G, m_offsets, total_m, P, N, K, {a_q, a_s}, {b_q, b_s},
+  return from_fp8(nvfp4::launch_fp8_wgrad(G, m_offsets, total_m, P, N, K, {a_q, a_s}, {b_q, b_s},
                                           fp8_out(dw, (int)dw_dtype, K, flags),
                                           (hipStream_t)stream));
 }

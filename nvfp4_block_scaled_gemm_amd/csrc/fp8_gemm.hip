@@ -167,11 +167,11 @@ hipError_t dense(int64_t M, int64_t N, int64_t K, Fp8Operand a, Fp8Operand b, Fp
                  hipStream_t stream) {
   using T = Tile<S::BM, S::BN, S::WM, S::WN, S::S, S::KG, BROWS, WIDE>;
   auto kern = fp8_dense_kernel<S::BM, S::BN, S::WM, S::WN, S::S, S::KG, BROWS, WIDE>;
+  const int64_t tiles = ((M + S::BM - 1) / S::BM) * ((N + S::BN - 1) / S::BN);
+  if (!grid_fits(tiles, T::kThreads)) return hipErrorNotSupported;
   static std::atomic<uint64_t> done{0};
   const hipError_t err = allow_lds(kern, T::kSmem, done);
   if (err != hipSuccess) return err;
-  const int64_t tiles = ((M + S::BM - 1) / S::BM) * ((N + S::BN - 1) / S::BN);
-  if (tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
   kern<<<(unsigned)tiles, T::kThreads, T::kSmem, stream>>>(M, N, K, a, b, y);
   return hipGetLastError();
 }
@@ -280,12 +280,13 @@ hipError_t wgrad(int32_t G, const int32_t* m_offsets, int64_t total_m, int64_t P
                  int64_t K, Fp8Operand a, Fp8Operand b, Fp8Out y, hipStream_t stream) {
   using T = Tile<S::BM, S::BN, S::WM, S::WN, S::S, 1, true, WIDE>;
   auto kern = fp8_wgrad_kernel<S::BM, S::BN, S::WM, S::WN, S::S, WIDE>;
+  const int64_t tiles = ((N + S::BM - 1) / S::BM) * ((K + S::BN - 1) / S::BN);
+  const int64_t per_group = (tiles + kXcds - 1) / kXcds * kXcds;
+  if (!grid_fits(per_group, T::kThreads) || !grid_fits(G * per_group, T::kThreads)) return hipErrorNotSupported;
+  const int64_t grid = G * per_group;
   static std::atomic<uint64_t> done{0};
   const hipError_t err = allow_lds(kern, T::kSmem, done);
   if (err != hipSuccess) return err;
-  const int64_t tiles = ((N + S::BM - 1) / S::BM) * ((K + S::BN - 1) / S::BN);
-  const int64_t grid = G * ((tiles + kXcds - 1) / kXcds) * kXcds;
-  if (tiles > 0x7FFFFFFF || grid > 0x7FFFFFFF) return hipErrorInvalidValue;
   kern<<<(unsigned)grid, T::kThreads, T::kSmem, stream>>>(G, m_offsets, total_m, P, N, K, a, b, y);
   return hipGetLastError();
 }

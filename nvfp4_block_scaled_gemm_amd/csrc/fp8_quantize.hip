@@ -340,13 +340,14 @@ hipError_t launch_fp8_quantize(const void* x, int dtype, int64_t batch, int64_t 
   const int64_t kblocks = (cols + kBlock - 1) / kBlock, rblocks = (rows + kBlock - 1) / kBlock;
   if (block_rows == 1 && qt == nullptr && batch == 1) {
     const int64_t grid = kblocks * ((rows + 16 * kRowPasses - 1) / (16 * kRowPasses));
-    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (!grid_fits(grid, 256)) return hipErrorNotSupported;
     auto kern = dtype == 1 ? quantize_rows_kernel<1, kRowPasses> : quantize_rows_kernel<0, kRowPasses>;
     kern<<<(unsigned)grid, 256, 0, stream>>>(x, rows, cols, ld_x, (int)kblocks, q, s);
     return hipGetLastError();
   }
-  const int64_t grid = batch * kblocks * rblocks;
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+  const int64_t tiles = kblocks * rblocks;  // below 2^47
+  if (!grid_fits(tiles, kTileThreads) || !grid_fits(batch * tiles, kTileThreads)) return hipErrorNotSupported;
+  const int64_t grid = batch * tiles;
   auto kern = block_rows == 1
                   ? (dtype == 1 ? quantize_tile_kernel<1, false> : quantize_tile_kernel<0, false>)
                   : (dtype == 1 ? quantize_tile_kernel<1, true> : quantize_tile_kernel<0, true>);
@@ -362,7 +363,7 @@ hipError_t launch_fp8_grouped_quantize(const void* x, int dtype, int32_t G,
   const int64_t P = fp8_padded_tokens(total_m, G);
   const int64_t kblocks = (cols + kBlock - 1) / kBlock;
   const int64_t grid = kblocks * (P / kBlock);
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (!grid_fits(grid, kTileThreads)) return hipErrorNotSupported;
   auto kern = dtype == 1 ? quantize_grouped_kernel<1> : quantize_grouped_kernel<0>;
   kern<<<(unsigned)grid, kTileThreads, 0, stream>>>(x, G, m_offsets, row_index, total_m, x_rows, cols, ld_x, P,
                                            (int)kblocks, q, s, qt, st);

@@ -255,7 +255,7 @@ template <int BM, int BN, int UNROLL, int WAVES, bool BROWS, bool WIDE>
 hipError_t stream_cfg(int64_t M, int64_t N, int64_t K, Fp8Operand a, Fp8Operand b, Fp8Out y,
                       hipStream_t stream) {
   const int64_t tiles = outputs<BM, BN>(M, N);
-  if (tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (!grid_fits(tiles, 64 * WAVES)) return hipErrorNotSupported;
   fp8_stream_kernel<BM, BN, UNROLL, WAVES, BROWS, WIDE>
       <<<(unsigned)tiles, 64 * WAVES, 0, stream>>>(M, N, K, a, b, y);
   return hipGetLastError();
@@ -315,7 +315,7 @@ hipError_t grouped_cfg(int32_t G, const int32_t* m_offsets, const int32_t* row_i
                        Fp8Operand b, Fp8Out y, hipStream_t stream) {
   // an expert ends at most one tile that is not full
   const int64_t tiles = (total_m / BM + (G < total_m ? G : total_m)) * ((N + BN - 1) / BN);
-  if (tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (!grid_fits(tiles, 64 * WAVES)) return hipErrorNotSupported;
   fp8_grouped_stream_kernel<BM, BN, UNROLL, WAVES, GATHER, WIDE>
       <<<(unsigned)tiles, 64 * WAVES, 0, stream>>>(G, m_offsets, row_index, total_m, a_rows, N, K, a, b, y);
   return hipGetLastError();

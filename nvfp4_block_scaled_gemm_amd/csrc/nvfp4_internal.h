@@ -124,6 +124,11 @@ struct Fp8Out {
   bool vec;    // rows start on 16-byte borders
 };
 
+// Whether a launch's threads fit the 32-bit count of a grid's dimension.  The
+// FP8 launchers answer hipErrorNotSupported where they do not, before any
+// other call.
+inline bool grid_fits(int64_t blocks, int64_t threads) { return blocks <= 0xFFFFFFFFll / threads; }
+
 // Columns of an expert-wise transposed operand: total_m tokens of G experts,
 // each expert's starting on a border of 128 (an upper bound known on the
 // host; the experts' counts are not).

@@ -114,6 +114,22 @@ def test_wgrad_checks(kw, status):
     assert _call("nvfp4_fp8_grouped_wgrad", WGRAD, kw) == status
 
 
+@pytest.mark.parametrize("name,defaults,kw", [
+    ("nvfp4_fp8_quantize", QUANT, dict(batch=1 << 24, rows=1, cols=16, ld_x=16, block_rows=128)),
+    ("nvfp4_fp8_quantize", QUANT, dict(rows=1 << 30, cols=1 << 20, ld_x=1 << 20)),
+    ("nvfp4_fp8_quantize", QUANT, dict(batch=1 << 30, rows=1 << 30, cols=1 << 30, ld_x=1 << 30)),
+    ("nvfp4_fp8_grouped_quantize", GQUANT, dict(total_m=1 << 30, x_rows=1 << 30, cols=1 << 14, ld_x=1 << 14)),
+    ("nvfp4_fp8_gemm", GEMM, dict(M=1, N=1 << 28, K=16, ld_y=1 << 28)),
+    ("nvfp4_fp8_gemm", GEMM, dict(M=2, N=1 << 27, K=4096, ld_y=1 << 27)),
+    ("nvfp4_fp8_gemm", GEMM, dict(M=1 << 30, N=16, K=16, ld_y=16, y_dtype=nv.NVFP4_BF16)),
+    ("nvfp4_fp8_grouped_gemm", GROUPED, dict(G=4, total_m=32, N=48 << 20, K=1 << 22, ld_y=48 << 20)),
+    ("nvfp4_fp8_grouped_wgrad", WGRAD, dict(G=1 << 25, N=16, K=16)),
+    ("nvfp4_fp8_grouped_wgrad", WGRAD, dict(G=1 << 30, N=1 << 30, K=1 << 30, dw_dtype=nv.NVFP4_BF16)),
+])
+def test_launches_past_a_grid_are_refused(name, defaults, kw):
+    assert _call(name, defaults, kw) == UNS
+
+
 ROUTE = dict(T=8, E=16, topk=2, logits=P, dtype=nv.NVFP4_F32, ld=16, mask=None, flags=0, expert_index=P,
              weights=P, counts=P, m_offsets=P, row_index=P, pair_row=P, routed=P, loss=P, workspace=P,
              workspace_bytes=1 << 20)
