@@ -718,11 +718,15 @@ size_t moe_route_workspace_bytes(int64_t T, int64_t E) {
 hipError_t launch_moe_route(int64_t T, int64_t E, int topk, const void* logits, int dtype,
                             int64_t ld, const uint8_t* mask, bool renorm, RouteOut out,
                             void* workspace, hipStream_t stream) {
-  // One workgroup takes the whole call where it needs about one turn for it
-  // (bf16, us, one launch and two: 1 x 256 top 8 6.3 / 9.4, 16 x 256 6.5 / 10.1,
-  // 64 x 128 8.5 / 9.4, 16 x 1024 top 16 13.0 / 17.7, 64 x 256 10.9 / 10.2, but
-  // 128 x 128 11.9 / 9.1, 64 x 512 top 10 16.1 / 12.2).
-  const bool one = T <= 64 && T * E <= 16384;
+  // One workgroup takes the whole call where it needs about one turn for it,
+  // and up to 256 experts only while the rounds of its 16 waves' choices do not
+  // outweigh the second launch (us, one launch and two, bf16 / fp32: 1 x 256
+  // top 8 6.2 / 9.5; 48 x 256 top 8 9.3 10.2 / 12.7 13.3; 64 x 256 top 2 9.5 9.8 / 9.7
+  // 10.2, but top 8 10.9 10.2 / 11.2 10.5 and top 16 12.8 11.1; 64 x 128 top 8
+  // 8.6 9.0 / 8.8 9.4, but top 16 9.8 9.8 / 10.3 9.8; 96 x 128 top 8 9.8 9.3; 32 x
+  // 512 top 16 12.4 13.2 / 13.0 13.6, but 48 x 512 14.8 13.2; 16 x 1024 top 16
+  // 12.8 18.2, but 32 x 1024 19.6 18.3).
+  const bool one = T <= 64 && T * E <= 16384 && (E > 256 || T * (E + 16 * topk) < 24576);
   const int64_t per = one ? T : chunk_tokens(T);
   const int chunks = one ? 1 : (int)((T + per - 1) / per);
   const Partials part = partials_at(workspace, chunks, E);

@@ -53,6 +53,16 @@ def test_route(T, E, k, dtype, renorm, masked):
     check(x, k, mask, renorm)
 
 
+@pytest.mark.parametrize("T,E,k", [(64, 256, 2), (64, 255, 7), (64, 256, 7), (48, 256, 15), (48, 256, 16), (64, 128, 16),
+                                   (64, 64, 16), (32, 512, 16), (33, 496, 4), (16, 1024, 1), (17, 1024, 1)])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_both_sides_of_one_launch(T, E, k, dtype):
+    x = logits_of(T, E, T * k + E, dtype)
+    note(f"route {T}x{E} top {k} {dtype}")
+    r, ref = check(x, k, torch.arange(T) % 5 != 3, True)
+    back(x, k, r, ref, torch.arange(T) % 5 != 3, True)
+
+
 @pytest.mark.parametrize("E", [8, 64, 256, 300, 1024])
 def test_ties_go_to_the_lowest_expert(E):
     x = torch.zeros(70, E)
