@@ -291,13 +291,19 @@ hipError_t stream_rows(int64_t M, int64_t N, int64_t K, Fp8Operand a, Fp8Operand
 // expected: one tile row for every expert that can have rows, or the rows'
 // worth and half a tile more for each.  16 x 16 while they do not fill the
 // card (2 experts with a row each, N = 1024, K = 4096: 6.2 us, 16 x 32 7.4,
-// 64 x 128 in the ring 16.4); 16 x 32 where one tile holds an expert's rows
-// and K is long enough for what a workgroup costs (us, this and the ring: 8
-// experts of 1 row, N = 4096, K = 2048 16.0 / 23.0; 2 of 1, 4096 x 14336 20.4 /
-// 94.7; 64 of 1, 1536 x 4096 60 / 83; but 32 of 1, 4096 x 2048 51.9 / 48.8, 32
-// of 4, 4096 x 1024 29.7 / 23.5); 32 x 32 for some more rows (8 of 16, 1024 x
-// 4096 10.9 / 31.0; 8 of 12, 4096 x 4096 29.1 / 31.2; 32 of 16, 1024 x 2048
-// 18.0 / 18.7; but 32 of 32, 1024 x 2048 28.6 / 19.9).
+// 64 x 128 in the ring 16.4).  Then 16 x 32 where one tile holds an expert's
+// rows, else 32 x 32, up to four workgroups a CU: all of them run at once, so
+// the time is little more than that of one loop over K.  Time in the ring over
+// the time here, K from 256 to 8192 (bf16; fp32 outputs):
+//   workgroups          256        512        1024       1280       2048
+//   16 x 32          1.5-3.3    1.3-1.9    1.1-1.3                0.7-1.3
+//               fp32 1.6-4.1    1.5-2.4    1.2-1.6                0.8-1.4
+//   32 x 32          1.3-2.8    1.5-1.7    0.9-1.2    0.8-1.2     0.6-1.0
+//               fp32 1.5-2.7    1.6-1.9    1.0-1.1    0.9-1.1     0.7-0.8
+// Above that a workgroup's start and end count: 16 x 32 keeps up with the
+// ring from K = 2048 on (2048 to 32768 workgroups: K = 2048 0.9-1.1, fp32
+// 1.0-1.2; K = 4096 1.0-1.3; K = 8192 0.95-1.04; but K = 1024 0.8-0.96, fp32
+// 0.9-1.07; K = 256 0.5-0.8), 32 x 32 never does.
 enum GroupedOutputs { kTiles, kRows16x16, kRows16x32, kRows32x32 };
 GroupedOutputs grouped_outputs(int64_t G, int64_t total_m, int64_t N, int64_t K) {
   const int64_t live = G < total_m ? G : total_m;
@@ -305,8 +311,9 @@ GroupedOutputs grouped_outputs(int64_t G, int64_t total_m, int64_t N, int64_t K)
   const int64_t more32 = total_m / 32 + live / 2, rows32 = more32 > live ? more32 : live;
   const int64_t n16 = (N + 15) / 16, n32 = (N + 31) / 32;
   if (rows * n16 <= kCUs) return kRows16x16;
-  if (rows * n32 <= kCUs || (more <= live && 2 * rows * n32 <= 3 * K)) return kRows16x32;
-  return rows32 * n32 <= 4 * kCUs && 2 * rows32 * n32 <= K ? kRows32x32 : kTiles;
+  if (rows * n32 <= kCUs) return kRows16x32;
+  if (more <= live) return rows * n32 <= 4 * kCUs || K >= 2048 ? kRows16x32 : kTiles;
+  return rows32 * n32 <= 4 * kCUs ? kRows32x32 : kTiles;
 }
 
 template <int BM, int BN, int UNROLL, int WAVES, bool GATHER, bool WIDE>
@@ -353,12 +360,15 @@ hipError_t launch_fp8_grouped_stream(int32_t G, const int32_t* m_offsets, const 
   return y.dtype == 0 ? go(std::true_type{}) : go(std::false_type{});
 }
 
-// Up to 16 rows the weights' stream is all that counts (us, here and in tiles:
-// 16 x 4096 x 4096 8.9 / 11.1, 16 x 8192 x 8192 17.2 / 20.2, 16 x 32768 x 2048
-// 17.1 / 20.2); otherwise as long as 32 x 32 outputs give every CU at most one
-// workgroup (64 x 4096 x 4096 11.3 / 13.4, 512 x 512 x 8192 17.7 / 16.9 and
-// with fp32 outputs 19.3 / 25.9; but 32 x 12288 x 4096 19.8 / 14.2, 128 x 4096 x
-// 2048 10.8 / 7.8).
+// Up to 16 rows the weights' stream is all that counts (us, here and in tiles,
+// bf16, then fp32 outputs: 1 x 16384 x 4096 15.7 16.7, 15.5 17.8; 16 x 4096 x 4096
+// 7.6 11.3, 7.3 15.0; 16 x 65536 x 4096 60 69, 63 69; the most against it: 16 x
+// 65536 x 2048 32.3 28.8, 32.5 33.1).  Otherwise as long as 32 x 32 outputs give
+// every CU at most one workgroup (64 x 4096 x 512 4.4 4.8, 4.6 5.5; 64 x 4096 x
+// 4096 11.1 13.6, 14.4 15.9; 512 x 512 x 8192 17.7 19.7, 22.3 26.6; the most
+// against it: 32 x 8192 x 4096 12.8 13.2, 16.0 15.6; past it 32 x 12288 x 4096
+// 20.3 15.8, 23.4 17.7; 128 x 4096 x 2048 11.0 8.6, 12.6 10.6; 512 x 1024 x 512
+// 5.3 5.0, 6.0 5.7).  So one border serves both types.
 bool fp8_streams(int64_t M, int64_t N) { return M <= 16 || outputs<32, 32>(M, N) <= kCUs; }
 
 hipError_t launch_fp8_stream(int64_t M, int64_t N, int64_t K, Fp8Operand a, Fp8Operand b,
