@@ -293,17 +293,21 @@ hipError_t stream_rows(int64_t M, int64_t N, int64_t K, Fp8Operand a, Fp8Operand
 // card (2 experts with a row each, N = 1024, K = 4096: 6.2 us, 16 x 32 7.4,
 // 64 x 128 in the ring 16.4).  Then 16 x 32 where one tile holds an expert's
 // rows, else 32 x 32, up to four workgroups a CU: all of them run at once, so
-// the time is little more than that of one loop over K.  Time in the ring over
-// the time here, K from 256 to 8192 (bf16; fp32 outputs):
-//   workgroups          256        512        1024       1280       2048
-//   16 x 32          1.5-3.3    1.3-1.9    1.1-1.3                0.7-1.3
-//               fp32 1.6-4.1    1.5-2.4    1.2-1.6                0.8-1.4
-//   32 x 32          1.3-2.8    1.5-1.7    0.9-1.2    0.8-1.2     0.6-1.0
-//               fp32 1.5-2.7    1.6-1.9    1.0-1.1    0.9-1.1     0.7-0.8
-// Above that a workgroup's start and end count: 16 x 32 keeps up with the
-// ring from K = 2048 on (2048 to 32768 workgroups: K = 2048 0.9-1.1, fp32
-// 1.0-1.2; K = 4096 1.0-1.3; K = 8192 0.95-1.04; but K = 1024 0.8-0.96, fp32
-// 0.9-1.07; K = 256 0.5-0.8), 32 x 32 never does.
+// the time is little more than that of one loop over K.  More workgroups have
+// their starts and ends to pay, those of experts without rows too, which 16 x 32
+// makes good while there are at most twice as many as elements of a long K.
+// Time in the ring over the time here, mean over routers' uneven rows (top 2 to
+// 8 of 8 to 256 experts, N = 512 to 4096), by workgroups up to
+//                 K    512  1024  2048  4096  8192  16384
+//   16 x 32     512   1.42  1.17  0.81  0.73  0.62   0.52
+//              2048   1.88  1.31  0.99  1.05  0.98   0.91
+//              4096   1.79  1.31  1.15  1.22  1.15   1.06
+//              6144   1.97  1.32  1.00  1.05  1.02   0.96
+//     fp32     2048   2.32  1.56  1.08  1.16  1.10   0.99
+//              6144   2.45  1.53  1.06  1.14  1.11   1.01
+//   32 x 32     512   1.40  1.13  0.73  0.58  0.43
+//              6144   1.81  1.28  0.86  0.70  0.47
+//     fp32     2048   1.86  1.26  0.84  0.65  0.46
 enum GroupedOutputs { kTiles, kRows16x16, kRows16x32, kRows32x32 };
 GroupedOutputs grouped_outputs(int64_t G, int64_t total_m, int64_t N, int64_t K) {
   const int64_t live = G < total_m ? G : total_m;
@@ -312,7 +316,7 @@ GroupedOutputs grouped_outputs(int64_t G, int64_t total_m, int64_t N, int64_t K)
   const int64_t n16 = (N + 15) / 16, n32 = (N + 31) / 32;
   if (rows * n16 <= kCUs) return kRows16x16;
   if (rows * n32 <= kCUs) return kRows16x32;
-  if (more <= live) return rows * n32 <= 4 * kCUs || K >= 2048 ? kRows16x32 : kTiles;
+  if (more <= live) return rows * n32 <= (K >= 2048 ? 2 * K : 4 * kCUs) ? kRows16x32 : kTiles;
   return rows32 * n32 <= 4 * kCUs ? kRows32x32 : kTiles;
 }
 

@@ -457,12 +457,13 @@ def test_grouped_many_tiles(counts, N, K, gather, out):
         close(y[rows], (a[0][src], a[1][:, src]), (b[0][e], b[1][e]), 128, out)
 
 
-@pytest.mark.parametrize("counts,N,K", [([1, 2, 0, 1] * 16, 4104, 2064), ([3, 1] * 12, 2100, 144), ([30, 26, 0, 41] * 2, 2056, 144),
+@pytest.mark.parametrize("counts,N,K", [([1, 2, 0, 1] * 16, 4104, 2064), ([1, 2, 0, 1] * 4, 4104, 2064), ([3, 1] * 12, 2100, 144),
+                                        ([30, 26, 0, 41] * 2, 2056, 144),
                                         ([30, 26, 0, 41] * 8, 2056, 400), ([2] * 40, 4104, 1040)])
 @pytest.mark.parametrize("gather", [False, True])
 @pytest.mark.parametrize("out", ["f32", "bf16"])
 def test_grouped_by_number_of_workgroups(counts, N, K, gather, out):
-    """Both sides of four workgroups a CU and of K = 2048, short and long K."""
+    """Both sides of four workgroups a CU, and of two for each element of K."""
     test_grouped_many_tiles(counts, N, K, gather, out)
 
 
