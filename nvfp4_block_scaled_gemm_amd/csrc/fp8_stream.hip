@@ -10,10 +10,10 @@
 // barrier in the loop, 16 bytes per lane and 64 contiguous bytes per row and
 // load -- and multiplies them as they arrive.  The waves' partial sums meet in
 // LDS at the end and are added in wave order, so results do not change
-// between calls.  Eight waves per 16 or 32 weight rows instead of one each:
-// at N = 8192 that is 4096 waves, 16 per CU, which is what it takes to keep
-// enough loads in flight: M = 1, N = K = 8192 reads its 67 MB at 4.4 TB/s
-// (15.3 us), 16384 x 4096 16.6 us, 4096 x 4096 7.1 us.
+// between calls.  Eight or sixteen waves per 16 or 32 weight rows instead of
+// one each are what it takes to keep enough loads in flight: M = 1, N = K =
+// 8192 reads its 67 MB by 512 workgroups of 16 waves in 13.6 us (4.9 TB/s; the
+// card reads 6.6 TB/s from a few GB in one launch), 4096 x 4096 takes 7.0 us.
 #include <type_traits>
 
 #include "fp8_tile.h"
@@ -269,17 +269,19 @@ template <bool BROWS, bool WIDE>
 hipError_t stream_rows(int64_t M, int64_t N, int64_t K, Fp8Operand a, Fp8Operand b, Fp8Out y,
                        hipStream_t stream) {
   // Outputs per workgroup: the smallest tile that still gives every CU at most
-  // one workgroup, since the time is then that of one loop over K (32 rows,
-  // N = 2048, K = 6144: 16 x 16 9.1 us, 16 x 32 11.4, 32 x 32 15.1; N = K =
-  // 4096: 11.6, 9.1, 11.0; M = 64: 18.3, 14.8, 11.2).  With more workgroups
+  // one workgroup, since the time is then that of one loop over K (bf16, 32
+  // rows, N = 2048, K = 6144: 16 x 16 8.9 us, 16 x 32 11.4, 32 x 32 14.9; N = K =
+  // 4096: 11.3, 9.1, 10.8; M = 64: 18.4, 14.7, 10.9).  With more workgroups
   // than CUs the re-reads of A decide: 16 weight rows a workgroup up to M = 8
-  // (N = K = 8192: M = 1 15.6, with 32 17.2), 32 from there (M = 16: 17.2,
-  // with 16 22.1).
+  // (N = K = 8192: M = 1 15.1, with 32 16.7; M = 8 16.9 and 17.0), 32 from there
+  // (M = 12: 17.0, with 16 19.1; M = 16: 17.0 and 21.1).
   const bool one16 = outputs<16, 16>(M, N) <= kCUs;
-  // Sixteen waves pay when a few rows leave the loop to loads' latency and
-  // each still has two blocks (M = 1, 4096 x 4096 7.7 -> 7.0 us, M = 16
-  // 7.7 -> 8.2; 2560 x 2048 4.1 -> 4.3).
-  if (M <= 4 && K >= 32 * kBlock)
+  // Sixteen waves pay when few rows leave a long loop to the loads' latency
+  // (M = 1, 16 and 8 waves: 12288 x 6144 15.7 / 16.6, 8192 x 8192 14.6 / 15.2, 4096
+  // x 14336 12.9 / 15.0, 2048 x 16384 12.7 / 14.9, though 5120 x 8192 13.8 / 13.0;
+  // M = 4 13.4 / 15.3 at 4096 x 14336; but 6144 x 4096 8.9 / 8.4, 14336 x 4096
+  // 15.1 / 15.0; 2560 x 2048 4.4 / 4.1; M = 9 16.9 / 17.0, in 16 x 32, at 8192 x 8192).
+  if (M <= 4 && K >= 48 * kBlock)
     return stream_cfg<16, 16, 2, 16, BROWS, true>(M, N, K, a, b, y, stream);
   if (M <= 8 || one16) return stream_cfg<16, 16, 4, 8, BROWS, true>(M, N, K, a, b, y, stream);
   if (M <= 16 || outputs<16, 32>(M, N) <= kCUs)

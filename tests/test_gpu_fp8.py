@@ -203,11 +203,11 @@ def test_gemm_accumulates(M, N, K, block_rows):
 
 
 @pytest.mark.parametrize("M", [1, 3, 4, 5])
-@pytest.mark.parametrize("N,K", [(300, 4096), (4099, 4112), (133, 8208), (72, 4080)])
+@pytest.mark.parametrize("N,K", [(300, 6144), (4099, 6160), (133, 8208), (72, 6128), (200, 4112)])
 @pytest.mark.parametrize("block_rows", [1, 128])
 @pytest.mark.parametrize("out,add", [("f32", False), ("f32", True), ("bf16", False)])
 def test_gemm_few_rows_of_long_k(M, N, K, block_rows, out, add):
-    """Both sides of the borders (4 rows, K = 4096) of the widest split of K;
+    """Both sides of the borders (4 rows, K = 6144) of the widest split of K;
     numbers of blocks that the waves do not share evenly, a last block cut."""
     rng = np.random.default_rng(M + N + K)
     a, b = rand_operand(rng, M, K), rand_operand(rng, N, K, block_rows)
@@ -219,7 +219,7 @@ def test_gemm_few_rows_of_long_k(M, N, K, block_rows, out, add):
 
 @pytest.mark.parametrize("M,N,K,block_rows", [(40, 1500, 272, 128), (500, 500, 272, 1), (600, 1500, 400, 128),
                                               (1024, 4100, 144, 128), (1024, 4100, 144, 1), (2000, 4100, 144, 128),
-                                              (2000, 4100, 144, 1), (2, 4099, 4112, 128)])
+                                              (2000, 4100, 144, 1), (2, 4099, 4112, 128), (2, 4099, 8208, 1)])
 def test_gemm_accumulates_in_every_shape(M, N, K, block_rows):
     rng = np.random.default_rng(M + N)
     a, b = rand_operand(rng, M, K), rand_operand(rng, N, K, block_rows)
@@ -291,7 +291,7 @@ def few_rows_close(y, a, b, block_rows, out):
     assert bad.size == 0, (bad[:4].tolist(), np_(y)[tuple(bad[0])], ref[tuple(bad[0])], tol[tuple(bad[0])])
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 300, 4112), (3, 128, 256), (5, 8200, 400), (16, 520, 2064), (20, 130, 400),
+@pytest.mark.parametrize("M,N,K", [(1, 300, 4112), (2, 300, 6160), (3, 128, 256), (5, 8200, 400), (16, 520, 2064), (20, 130, 400),
                                    (30, 4000, 272)])
 @pytest.mark.parametrize("block_rows", [1, 128])
 @pytest.mark.parametrize("out", ["f32", "bf16"])
