@@ -401,7 +401,7 @@ size_t nvfp4_moe_route_workspace_bytes(int64_t T, int64_t E);
  * grouped GEMMs take.
  *   p[t, :]      = softmax(logits[t, :])
  *   expert_index int32 [T, topk]  experts of the largest logits, descending,
- *                ties to the lowest expert
+ *                ties (-0 and +0 too) to the lowest expert
  *   weights      fp32 [T, topk]   p at those (or, renormalised, their softmax)
  *   counts       int32 [E]        tokens of each expert
  *   m_offsets    int32 [E + 1]    their running sums

@@ -56,7 +56,10 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void fp8_dense_kernel(int64_t
 // Experts' products: workgroups walk the list of (expert, tile column, tile
 // row) tiles, tile rows fastest so that neighbours share a weight tile.  The
 // list is known on the device only: each wave keeps 64 experts' running tile
-// counts in its lanes and finds a tile's expert by one ballot.
+// counts in its lanes and finds a tile's expert by one ballot.  (In the 256 x
+// 256 shape that walk costs three spilled registers, stored once and read again
+// before and after each tile's loop over K, never in it; the dense kernel of
+// the shape has none.)
 template <int BM, int BN, int WM, int WN, int STAGES, bool GATHER, bool WIDE>
 __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_grouped_kernel(
     int G, const int32_t* __restrict__ offsets, const int32_t* __restrict__ row_index,

@@ -31,10 +31,12 @@
 // write); the chosen weights' gradients meet their experts through LDS.
 //
 // The choice is bound by the vector unit (1.5 k instructions a logit besides
-// the softmax's), the rest by launches and latency.  Measured,
-// bf16, 256 experts, top 8: 1 token 6.3 us forward and 3.3 backward, 4096
-// tokens 16.2 and 4.2, 65536 40.7 (34 MB of logits; of it the choice 28) and
-// 17.2 (67 MB, 3.9 TB/s).
+// the softmax's); of the placement, each workgroup's reading of all chunks'
+// counts (256 KB from L2 at 65536 x 256) before it places a token; the rest by
+// launches.  Measured, bf16, 256 experts, top 8, replayed from a graph: 1 token
+// 6.1 us forward and 3.5 backward, 4096 tokens 15.9 and 4.3, 65536 38.0 (34 MB
+// of logits) and 17.9 (67 MB, 3.7 TB/s); there, profiled one kernel at a time,
+// choice 29, placement 12 and backward 21.
 #include "nvfp4_device.h"
 #include "nvfp4_internal.h"
 
