@@ -90,14 +90,15 @@ __device__ __forceinline__ float group_sum(float v) {
 // exp(d), d <= 0, within 2^-22 relative however far d is.  The instruction
 // raises 2 to t = d log2(e), whose rounding alone is up to 2^-24 |t| (5e-6 of
 // the result at d = -88): what t loses is kept in r and put back as
-// 2^t (1 + r ln 2).  Zero from d = -200 on, where -inf would have no r.
+// 2^t (1 + r ln 2).  |r| stays below 2^-16 wherever 2^t is not 0; the bounds
+// keep it a number where t is -inf (a median drops a NaN of its arguments), and
+// a NaN in d comes out through 2^t.
 __device__ __forceinline__ float exp_below(float d) {
   constexpr float kLog2e = 1.44269502f, kLog2eRest = 1.92596303e-8f, kLn2 = 0.693147181f;
-  d = fmaxf(d, -200.0f);
   const float t = d * kLog2e;
   const float r = __builtin_fmaf(d, kLog2eRest, __builtin_fmaf(d, kLog2e, -t));
   const float y = __builtin_amdgcn_exp2f(t);
-  return __builtin_fmaf(y, r * kLn2, y);
+  return __builtin_fmaf(y, __builtin_amdgcn_fmed3f(r, -1.0f, 1.0f) * kLn2, y);
 }
 
 // A logit as fp32.

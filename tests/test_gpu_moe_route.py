@@ -137,6 +137,24 @@ def test_far_logits_keep_fp32_weights_and_gradients(T, E, k, dtype, renorm):
     assert np.abs(got[rest] / want[rest] - 1).max() <= 2 * rel
 
 
+@pytest.mark.parametrize("T", [8, 300])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_a_nan_logit_shows_in_its_token_alone(T, renorm, dtype):
+    """NaN is outside the contract, but must not turn into a plausible weight;
+    logits at the lowest value and at -inf beside it stay zeros."""
+    x = logits_of(T, 20, 6, dtype)
+    x[1, 3], x[2, 5:], x[3, 5:] = float("nan"), torch.finfo(x.dtype).min, -float("inf")
+    x = x.to(DEV)
+    note(f"route nan logit T {T} renorm {renorm} {dtype}")
+    r = nv.nvfp4_moe_route(x, 3, renormalize=renorm)
+    g = nv.nvfp4_moe_route_backward(x, r, torch.ones(T, 3, device=DEV), torch.ones(1, device=DEV), renormalize=renorm)
+    rest = torch.arange(T, device=DEV) != 1
+    assert bool(r.weights[1].isnan().all()) and bool(r.weights[rest].isfinite().all())
+    assert bool(g[1].isnan().any()) and bool(g[rest].isfinite().all())
+    assert not bool(g[2:4, 5:].any())
+
+
 def test_all_masked_and_no_tokens():
     note("route with no token")
     for x, mask in ((logits_of(9, 12, 1, "fp32"), torch.zeros(9, dtype=torch.bool)),
