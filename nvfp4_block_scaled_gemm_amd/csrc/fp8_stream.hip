@@ -262,9 +262,11 @@ hipError_t stream_cfg(int64_t M, int64_t N, int64_t K, Fp8Operand a, Fp8Operand 
 }
 
 // WIDE: how 32-row tiles multiply.  16-row tiles always take the 16-bit
-// instructions and their fp32 sums, bf16 outputs too: the loads hide them (us,
-// 8-bit and wide: 1 x 8192 x 8192 14.6 / 14.6, 16 x 4096 x 4096 7.6 / 7.5, 32 x
-// 4096 x 4096 8.9 / 9.2; of 32-row tiles 64 x 4096 x 4096 10.9 / 14.3).
+// instructions and their fp32 sums, bf16 outputs too: the loads hide them, or
+// most of them (us, 8-bit and wide: 1 x 8192 x 8192 14.6 / 14.6, 16 x 4096 x 4096
+// 7.6 / 7.5, 32 x 4096 x 4096 8.9 / 9.2, 16 x 32768 x 4096 30.8 / 32.5; experts, 16
+// tokens top 2 of 8, 4096 x 14336 83 / 87; of 32-row tiles 64 x 4096 x 4096 10.9 /
+// 14.3).
 template <bool BROWS, bool WIDE>
 hipError_t stream_rows(int64_t M, int64_t N, int64_t K, Fp8Operand a, Fp8Operand b, Fp8Out y,
                        hipStream_t stream) {

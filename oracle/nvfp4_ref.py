@@ -20,8 +20,8 @@ What the pages fix
 * leverageai "blackwell-nvfp4-gemm-optimization", "What is this?":
   quantisation may happen ahead of execution and is timed apart from the GEMM.
 
-Readings where the pages are silent (each is listed in the design doc)
-----------------------------------------------------------------
+Readings where the pages are silent
+-----------------------------------
 R1  E2M1 magnitudes are {0, .5, 1, 1.5, 2, 3, 4, 6} for codes 0..7 (bits 0-2
     of a nibble), bit 3 is the sign.
 R2  E4M3FN: sign bit 7, exponent bits 6-3 (bias 7), mantissa bits 2-0;
