@@ -1,27 +1,12 @@
 // FP8 block-128 products: dense, per expert, and the experts' weight
 // gradients.  The tile itself is in fp8_tile.h; here is which tile a
 // workgroup takes.
-#include <atomic>
-
-#include "fp8_tile.h"
-#include "nvfp4_internal.h"
+#include "fp8_launch.h"
 
 namespace nvfp4 {
 namespace {
 
 using namespace fp8;
-
-constexpr int kXcds = 8;
-
-__device__ __forceinline__ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-// Hardware workgroup ids go round-robin over the XCDs; a bijection that
-// gives each XCD a run of neighbouring logical ids (shared rows in its L2).
-__device__ __forceinline__ int xcd_run(int pid, int n) {
-  const int per = n / kXcds, extra = n % kXcds;
-  const int x = pid % kXcds, i = pid / kXcds;
-  return x * per + min(x, extra) + i;
-}
 
 // Rows [r0, r0 + rows) of a whole operand as a tile operand.
 __device__ __forceinline__ TileOperand rows_of(const uint8_t* q, const float* s, int64_t s_ld,
@@ -140,31 +125,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_wgrad_kernel(
   T::template run<false>(A, B, (uint32_t)len, (uint32_t)P, out_of(y, ((int64_t)e * N + m0) * K + n0, rm, rn), smem);
 }
 
-// Allows a kernel its LDS, once per kernel and device.
-template <typename Kern>
-hipError_t allow_lds(Kern kern, int bytes, std::atomic<uint64_t>& done) {
-  int dev = 0;
-  hipError_t e = hipGetDevice(&dev);
-  if (e != hipSuccess) return e;
-  const uint64_t bit = 1ull << (dev & 63);
-  if (done.load(std::memory_order_acquire) & bit) return hipSuccess;
-  e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == hipSuccess) done.fetch_or(bit, std::memory_order_release);
-  return e;
-}
-
-// A tile shape: BM x BN outputs by WM x WN waves with a ring of S stages.
-template <int BM_, int BN_, int WM_, int WN_, int S_, int KG_ = 1>
-struct Shape {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_, KG = KG_;
-};
-using S256x256 = Shape<256, 256, 2, 4, 2>;
-using S128x256 = Shape<128, 256, 2, 4, 3>;
-using S128x128 = Shape<128, 128, 2, 2, 2>;
-using S128x64 = Shape<128, 64, 2, 2, 3, 2>;
-using S64x128 = Shape<64, 128, 2, 2, 3>;
-using S64x64 = Shape<64, 64, 2, 2, 3, 2>;
-
 template <typename S, bool BROWS, bool WIDE>
 hipError_t dense(int64_t M, int64_t N, int64_t K, Fp8Operand a, Fp8Operand b, Fp8Out y,
                  hipStream_t stream) {
@@ -177,22 +137,6 @@ hipError_t dense(int64_t M, int64_t N, int64_t K, Fp8Operand a, Fp8Operand b, Fp
   if (err != hipSuccess) return err;
   kern<<<(unsigned)tiles, T::kThreads, T::kSmem, stream>>>(M, N, K, a, b, y);
   return hipGetLastError();
-}
-
-// Time of a shape in units of 0.01 us per block of K, from the tiles that the
-// busiest of 256 CUs gets: t1 for one tile alone on a CU, t2 for two (shapes
-// of which one fits a CU: twice t1).
-int64_t tiles_cost(int64_t tiles, int64_t t1, int64_t t2) {
-  const int64_t n = (tiles + 255) / 256;
-  return n / 2 * t2 + n % 2 * t1;
-}
-
-int64_t tiles_of(int64_t rows, int64_t cols, int64_t bm, int64_t bn) {
-  return ((rows + bm - 1) / bm) * ((cols + bn - 1) / bn);
-}
-
-int64_t shape_cost(int64_t M, int64_t N, int64_t bm, int64_t bn, int64_t t1, int64_t t2) {
-  return tiles_cost(tiles_of(M, N, bm, bn), t1, t2);
 }
 
 // The shape with the least expected time.  Measured (us per block of 128,
