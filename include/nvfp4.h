@@ -389,6 +389,152 @@ int nvfp4_fp8_grouped_wgrad(int32_t G, const int32_t* m_offsets, int64_t total_m
                             const float* b_s, void* dw, nvfp4_dtype dw_dtype, unsigned flags,
                             void* stream);
 
+/* Activation of a gated block: act(g) = g sigma(z), with z = g (SILU) or
+ * z = 2 sqrt(2/pi) (g + 0.044715 g^3) (GELU, the tanh form). */
+typedef enum {
+  NVFP4_SILU = 0,
+  NVFP4_GELU = 1
+} nvfp4_act;
+
+/*
+ * Gated feed-forward block, first half: h = act(x Wg^T) * (x Wu^T) [M, F] in one
+ * product of the FP8 operands a = x [M, K] (block_rows 1) and w = [Wg; Wu]
+ * [2F, K] (gate rows first; w_block_rows 1 or 128; F of any size, though a
+ * block of 128 rows that ends inside the gate's last 32 costs some time).
+ * Both products are summed as in nvfp4_fp8_gemm with an output of h's type
+ * and stay in fp32 up to h, which is rounded once.  gate_up (or NULL): bf16
+ * [M, 2F], the two products for the backward.  h (F32 or BF16) has row stride
+ * ld_h >= F, gate_up ld_gate_up >= 2F elements.  K == 0 writes zeros.
+ * Errors as nvfp4_fp8_gemm (2F in the place of N), and
+ * NVFP4_ERR_INVALID_ARG for a bad act, NVFP4_ERR_UNSUPPORTED for F > 2^27.
+ */
+int nvfp4_fp8_gated_gemm(int64_t M, int64_t F, int64_t K, const uint8_t* a_q, const float* a_s,
+                         const uint8_t* w_q, const float* w_s, int w_block_rows, nvfp4_act act,
+                         void* h, nvfp4_dtype h_dtype, int64_t ld_h, void* gate_up,
+                         int64_t ld_gate_up, void* stream);
+
+/*
+ * The same per expert: group e's rows of a times w_q + e*2F*K,
+ * w_s [G, ceil(K/128), ceil(2F/128)] (block_rows 128), with m_offsets, row_index
+ * and a_rows as in nvfp4_fp8_grouped_gemm.  Rows of h and gate_up of no group
+ * are left as they were.
+ */
+int nvfp4_fp8_grouped_gated_gemm(int32_t G, const int32_t* m_offsets, const int32_t* row_index,
+                                 int64_t total_m, int64_t a_rows, int64_t F, int64_t K,
+                                 const uint8_t* a_q, const float* a_s, const uint8_t* w_q,
+                                 const float* w_s, nvfp4_act act, void* h, nvfp4_dtype h_dtype,
+                                 int64_t ld_h, void* gate_up, int64_t ld_gate_up, void* stream);
+
+/*
+ * Its backward: from dh [rows, F] and gate_up = [g, u] [rows, 2F] (F32 or BF16
+ * each)
+ *   dg = dh u act'(g),   du = dh act(g)
+ * as the FP8 operand [dg, du] [rows, 2F] of the products that follow, in either
+ * or both layouts of nvfp4_fp8_quantize (block_rows 1):
+ *   dx = [dg, du] . W       a = rows layout, b = W (128, transposed [K, 2F])
+ *   dW = [dg, du]^T . x     a = transposed,  b = x (transposed)
+ * dg and du are fp32 up to that quantisation.
+ * Errors: NVFP4_ERR_INVALID_ARG for F % 8 != 0, negative sizes, a bad dtype or
+ * act, a row stride below the row, one pointer of a pair without the other,
+ * both pairs null, or a null input; NVFP4_ERR_UNSUPPORTED for inputs, their
+ * rows, q or qt not 16-byte aligned, F > 2^27, rows above 2^30, or sizes whose
+ * launch would pass 2^32 threads.
+ */
+int nvfp4_fp8_gated_backward(const void* dh, nvfp4_dtype dh_dtype, int64_t ld_dh,
+                             const void* gate_up, nvfp4_dtype gate_up_dtype, int64_t ld_gate_up,
+                             nvfp4_act act, int64_t rows, int64_t F, uint8_t* q, float* s,
+                             uint8_t* qt, float* st, void* stream);
+
+/*
+ * The same for rows sorted by group: layouts, padding columns and rows of no
+ * group as in nvfp4_fp8_grouped_quantize (cols = 2F), for
+ * nvfp4_fp8_grouped_gemm and nvfp4_fp8_grouped_wgrad.
+ */
+int nvfp4_fp8_grouped_gated_backward(int32_t G, const int32_t* m_offsets, const void* dh,
+                                     nvfp4_dtype dh_dtype, int64_t ld_dh, const void* gate_up,
+                                     nvfp4_dtype gate_up_dtype, int64_t ld_gate_up, nvfp4_act act,
+                                     int64_t total_m, int64_t F, uint8_t* q, float* s, uint8_t* qt,
+                                     float* st, void* stream);
+
+/*
+ * 8-bit integers with one fp32 scale per row, for serving: exact sums, and a
+ * scale for each token and each output channel.
+ *   q  int8 [rows, K]  dense rows
+ *   s  fp32 [rows]     an element decodes as q[r, k] * s[r]
+ *
+ * nvfp4_int8_quantize: x [rows, cols] (F32 or BF16, row stride ld_x) -> q, s.
+ * Per row: A = max(max|x|, 2^-100), s = fl32(A / 127), each q is
+ * fl32(x * fl32(127 / A)) rounded to the nearest integer, ties to even.  A row
+ * holding a NaN or an infinity gets a NaN scale and zeros.  Deterministic.
+ * Errors: NVFP4_ERR_INVALID_ARG for cols % 16 != 0, negative sizes, a bad
+ * dtype, ld_x < cols or a null pointer; NVFP4_ERR_UNSUPPORTED for x, its rows
+ * or q not 16-byte aligned, s not 4-byte aligned, a dimension above 2^30, or
+ * sizes whose launch would pass 2^32 threads.
+ */
+int nvfp4_int8_quantize(const void* x, nvfp4_dtype x_dtype, int64_t rows, int64_t cols,
+                        int64_t ld_x, int8_t* q, float* s, void* stream);
+
+/*
+ * y[m, n] = fl32(sum_k a_q[m, k] b_q[n, k]) * a_s[m] * b_s[n] (in this order) of
+ * INT8 operands a [M, K] and b = W [N, K].  The sum is an exact 32-bit integer.
+ * y [M, N] (F32 or BF16) has row stride ld_y >= N.  A NaN scale gives NaN in
+ * its row (column).  K == 0 writes zeros.
+ * Errors: NVFP4_ERR_INVALID_ARG for K % 16 != 0, negative sizes, a bad dtype,
+ * ld_y < N or a null pointer; NVFP4_ERR_UNSUPPORTED for q not 16-byte aligned,
+ * s or y not aligned to their elements, K >= 2^17 (where a sum could pass 32
+ * bits), another dimension above 2^30, or sizes whose launch would pass 2^32
+ * threads.
+ */
+int nvfp4_int8_gemm(int64_t M, int64_t N, int64_t K, const int8_t* a_q, const float* a_s,
+                    const int8_t* b_q, const float* b_s, void* y, nvfp4_dtype y_dtype,
+                    int64_t ld_y, void* stream);
+
+/* One gradient of a list: n dense elements at g, and where its clipped values
+ * go (out NULL or g: in place, out_dtype then being g_dtype). */
+typedef struct nvfp4_grad {
+  void* g;   /* DEVICE */
+  void* out; /* DEVICE */
+  int64_t n;
+  nvfp4_dtype g_dtype;
+  nvfp4_dtype out_dtype;
+} nvfp4_grad;
+
+/* Bytes of device workspace of the two calls below for a list of `count`. */
+size_t nvfp4_grad_workspace_bytes(int64_t count);
+
+/*
+ * Sum of the squares of all elements of a list of gradients -> norm_sq (DEVICE,
+ * one IEEE binary64).  `grads` is a HOST array, read before the call returns;
+ * `out` is not read.  Squares and sums are binary64, so nothing finite
+ * overflows; their order depends on the list's sizes, types and addresses
+ * alone.  A caller whose gradients are spread over processes adds their sums
+ * before it clips.  workspace >= nvfp4_grad_workspace_bytes(count) bytes, 8-byte
+ * aligned, not shared by calls that may overlap.  count == 0 writes 0.
+ * Errors: NVFP4_ERR_INVALID_ARG for count < 0, n < 0, a bad dtype, a null
+ * pointer (g only where n > 0) or a workspace too small;
+ * NVFP4_ERR_UNSUPPORTED for pointers not aligned to their elements, or more
+ * than 2^42 elements or 2^20 tensors.
+ */
+int nvfp4_grad_norm_sq(int64_t count, const nvfp4_grad* grads, double* norm_sq, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/*
+ * out = g * c with c = max_norm / norm where norm > max_norm, else 1, and
+ * norm = sqrt(norm_sq).  norm_sq (DEVICE, or NULL: it is computed from the list)
+ * may be a sum over several processes.  norm (DEVICE fp32, or NULL) receives the
+ * norm before clipping.  c and the product are binary64, rounded to fp32 (and
+ * from there to bf16) as out is written.  With c == 1 gradients in place are not
+ * touched, others are copied; a norm_sq that is not finite counts as c == 1, so
+ * that a step can be dropped by looking at norm.  max_norm >= 0 (infinity: never
+ * clips).
+ * Errors: as above, and NVFP4_ERR_INVALID_ARG for max_norm < 0 or NaN, types
+ * that differ in place, or a written tensor that overlaps another one of the
+ * list; workspace may be NULL where norm_sq is given.
+ */
+int nvfp4_clip_grads(int64_t count, const nvfp4_grad* grads, double max_norm,
+                     const double* norm_sq, float* norm, void* workspace, size_t workspace_bytes,
+                     void* stream);
+
 /* nvfp4_moe_route flag: weights are the softmax over the chosen experts. */
 #define NVFP4_ROUTE_RENORMALIZE 1u
 

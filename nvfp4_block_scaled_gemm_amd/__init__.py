@@ -1,7 +1,8 @@
 """MI355X (gfx950) NVFP4 block-scaled GEMM: y = x . W^T with E2M1 operands,
 E4M3FN scales per 16 elements and fp32 per-tensor global scales; MXFP4 and
 FP8 (E4M3, one fp32 scale per 128) variants, grouped products for experts and
-the router that orders their tokens.
+the router that orders their tokens; gated feed-forward blocks on FP8, INT8
+products, and the norm and clipping of gradients.
 
 The computation lives in ``libnvfp4.so`` (HIP kernels + C ABI, declared in
 ``include/nvfp4.h``); this package only marshals torch tensors into it.
@@ -20,4 +21,11 @@ from ._lib import (  # noqa: F401
     nvfp4_fp8_grouped_wgrad, nvfp4_fp8_grouped_wgrad_raw, nvfp4_fp8_quantize,
     nvfp4_fp8_quantize_raw, nvfp4_moe_route, nvfp4_moe_route_backward,
     nvfp4_moe_route_backward_raw, nvfp4_moe_route_raw, nvfp4_moe_route_workspace_bytes,
+    Grad, Int8Packed, NVFP4_GELU, NVFP4_SILU, nvfp4_clip_grads, nvfp4_clip_grads_raw,
+    nvfp4_fp8_gated_backward, nvfp4_fp8_gated_backward_raw, nvfp4_fp8_gated_gemm,
+    nvfp4_fp8_gated_gemm_raw, nvfp4_fp8_grouped_gated_backward,
+    nvfp4_fp8_grouped_gated_backward_raw, nvfp4_fp8_grouped_gated_gemm,
+    nvfp4_fp8_grouped_gated_gemm_raw, nvfp4_grad_norm_sq, nvfp4_grad_norm_sq_raw,
+    nvfp4_grad_workspace_bytes, nvfp4_int8_gemm, nvfp4_int8_gemm_raw, nvfp4_int8_quantize,
+    nvfp4_int8_quantize_raw,
 )

@@ -7,6 +7,7 @@ there is no fallback implementation.
 """
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
 import functools
@@ -32,9 +33,13 @@ EXPORTED = ("nvfp4_status_string", "nvfp4_version", "nvfp4_quantize_workspace_by
             "nvfp4_mxfp4_gemm", "nvfp4_fp8_quantize", "nvfp4_fp8_grouped_columns",
             "nvfp4_fp8_grouped_quantize", "nvfp4_fp8_gemm", "nvfp4_fp8_grouped_gemm",
             "nvfp4_fp8_grouped_wgrad", "nvfp4_moe_route_workspace_bytes", "nvfp4_moe_route",
-            "nvfp4_moe_route_backward")
+            "nvfp4_moe_route_backward", "nvfp4_fp8_gated_gemm", "nvfp4_fp8_grouped_gated_gemm",
+            "nvfp4_fp8_gated_backward", "nvfp4_fp8_grouped_gated_backward", "nvfp4_int8_quantize",
+            "nvfp4_int8_gemm", "nvfp4_grad_workspace_bytes", "nvfp4_grad_norm_sq", "nvfp4_clip_grads")
 NVFP4_ACCUMULATE = 1
 NVFP4_ROUTE_RENORMALIZE = 1
+NVFP4_SILU = 0
+NVFP4_GELU = 1
 NVFP4_GROUPED_MAX_PROBLEMS = 4
 
 _lib = None
@@ -48,6 +53,12 @@ class GroupedProblem(ctypes.Structure):
                 ("a_q", ctypes.c_void_p), ("a_s", ctypes.c_void_p), ("a_g", ctypes.c_void_p),
                 ("b_q", ctypes.c_void_p), ("b_s", ctypes.c_void_p), ("b_g", ctypes.c_void_p),
                 ("y", ctypes.c_void_p), ("y_dtype", ctypes.c_int), ("ld_y", ctypes.c_int64)]
+
+
+class Grad(ctypes.Structure):
+    """nvfp4_grad of include/nvfp4.h (one gradient of a list)."""
+    _fields_ = [("g", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("g_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int)]
 
 
 class Nvfp4Error(RuntimeError):
@@ -117,6 +128,26 @@ def load() -> ctypes.CDLL:
     lib.nvfp4_moe_route_backward.argtypes = [i64, i64, i32, p, c_int, i64, p, c_uint, p, p, p, p, p,
                                              p, i64, p]
     lib.nvfp4_moe_route_backward.restype = c_int
+    lib.nvfp4_fp8_gated_gemm.argtypes = [i64, i64, i64, p, p, p, p, c_int, c_int, p, c_int, i64, p, i64, p]
+    lib.nvfp4_fp8_gated_gemm.restype = c_int
+    lib.nvfp4_fp8_grouped_gated_gemm.argtypes = [i32, p, p, i64, i64, i64, i64, p, p, p, p, c_int, p, c_int,
+                                                 i64, p, i64, p]
+    lib.nvfp4_fp8_grouped_gated_gemm.restype = c_int
+    lib.nvfp4_fp8_gated_backward.argtypes = [p, c_int, i64, p, c_int, i64, c_int, i64, i64, p, p, p, p, p]
+    lib.nvfp4_fp8_gated_backward.restype = c_int
+    lib.nvfp4_fp8_grouped_gated_backward.argtypes = [i32, p, p, c_int, i64, p, c_int, i64, c_int, i64, i64, p,
+                                                     p, p, p, p]
+    lib.nvfp4_fp8_grouped_gated_backward.restype = c_int
+    lib.nvfp4_int8_quantize.argtypes = [p, c_int, i64, i64, i64, p, p, p]
+    lib.nvfp4_int8_quantize.restype = c_int
+    lib.nvfp4_int8_gemm.argtypes = [i64, i64, i64, p, p, p, p, p, c_int, i64, p]
+    lib.nvfp4_int8_gemm.restype = c_int
+    lib.nvfp4_grad_workspace_bytes.argtypes = [i64]
+    lib.nvfp4_grad_workspace_bytes.restype = sz
+    lib.nvfp4_grad_norm_sq.argtypes = [i64, p, p, p, sz, p]
+    lib.nvfp4_grad_norm_sq.restype = c_int
+    lib.nvfp4_clip_grads.argtypes = [i64, p, ctypes.c_double, p, p, p, sz, p]
+    lib.nvfp4_clip_grads.restype = c_int
     _lib = lib
     return lib
 
@@ -552,7 +583,7 @@ def _here(stream, dev: int) -> bool:
 def _stride(t, cols: int, what: str) -> int:
     """Row stride of a 2-D tensor whose rows must be contiguous (a single
     row's stride says nothing, so its length stands in)."""
-    _need(t.stride(-1) == 1 or cols <= 1, f"{what}: rows must have unit column stride")
+    _need(t.stride(-1) == 1 or cols <= 1 or t.numel() == 0, f"{what}: rows must have unit column stride")
     return t.stride(-2) if t.shape[-2] > 1 else cols
 
 
@@ -969,3 +1000,352 @@ def nvfp4_moe_route_backward(logits: torch.Tensor, route: MoeRoute,
                                           _stride(out, E, "out"), _stream(None, dev))
     _check("nvfp4_moe_route_backward", st)
     return out
+
+
+# --------------------------------------------------------------------------
+# gated feed-forward blocks on FP8 operands
+# --------------------------------------------------------------------------
+
+_ACT = {"silu": NVFP4_SILU, "gelu": NVFP4_GELU}
+
+
+def nvfp4_fp8_gated_gemm_raw(M, F, K, a_q, a_s, w_q, w_s, w_block_rows, act, h, h_dtype, ld_h, gate_up,
+                             ld_gate_up, stream=None) -> int:
+    return load().nvfp4_fp8_gated_gemm(M, F, K, a_q, a_s, w_q, w_s, w_block_rows, act, h, h_dtype, ld_h,
+                                       gate_up, ld_gate_up, _stream(stream))
+
+
+def nvfp4_fp8_grouped_gated_gemm_raw(G, m_offsets, row_index, total_m, a_rows, F, K, a_q, a_s, w_q, w_s, act,
+                                     h, h_dtype, ld_h, gate_up, ld_gate_up, stream=None) -> int:
+    return load().nvfp4_fp8_grouped_gated_gemm(G, m_offsets, row_index, total_m, a_rows, F, K, a_q, a_s, w_q,
+                                               w_s, act, h, h_dtype, ld_h, gate_up, ld_gate_up,
+                                               _stream(stream))
+
+
+def nvfp4_fp8_gated_backward_raw(dh, dh_dtype, ld_dh, gate_up, gate_up_dtype, ld_gate_up, act, rows, F, q, s,
+                                 qt, st, stream=None) -> int:
+    return load().nvfp4_fp8_gated_backward(dh, dh_dtype, ld_dh, gate_up, gate_up_dtype, ld_gate_up, act, rows,
+                                           F, q, s, qt, st, _stream(stream))
+
+
+def nvfp4_fp8_grouped_gated_backward_raw(G, m_offsets, dh, dh_dtype, ld_dh, gate_up, gate_up_dtype, ld_gate_up,
+                                         act, total_m, F, q, s, qt, st, stream=None) -> int:
+    return load().nvfp4_fp8_grouped_gated_backward(G, m_offsets, dh, dh_dtype, ld_dh, gate_up, gate_up_dtype,
+                                                   ld_gate_up, act, total_m, F, q, s, qt, st, _stream(stream))
+
+
+def _act(act: str) -> int:
+    code = _ACT.get(act)
+    _need(code is not None, "act: 'silu' or 'gelu'")
+    return code
+
+
+def _gate_up(gate_up, rows: int, F: int, like, dev: int):
+    """The kept products' buffer and row stride (None, 0: not wanted)."""
+    if gate_up is None or gate_up is False:
+        return None, 0
+    if gate_up is True:
+        return like.new_empty((rows, 2 * F), dtype=torch.bfloat16), 2 * F
+    _need(gate_up.dtype == torch.bfloat16 and tuple(gate_up.shape) == (rows, 2 * F),
+          f"gate_up: expected bf16 ({rows}, {2 * F})")
+    _on_dev(gate_up, dev, "gate_up")
+    return gate_up, _stride(gate_up, 2 * F, "gate_up")
+
+
+def nvfp4_fp8_gated_gemm(a, w, act: str = "silu", out_dtype: str = "bf16", h: torch.Tensor | None = None,
+                         gate_up=None, stream=None):
+    """a = Fp8Packed [M, K] with block_rows 1; w = Fp8Packed [2F, K] (gate rows,
+    then up rows) with block_rows 1 or 128 -> h [M, F] = act(a . Wg^T) * (a .
+    Wu^T), act "silu" or "gelu" (tanh form).  gate_up: True, or a bf16 [M, 2F]
+    buffer, keeps the two products for nvfp4_fp8_gated_backward; the answer is
+    then (h, gate_up).  ``h`` reuses a buffer of out_dtype, whose sums are as
+    nvfp4_fp8_gemm's."""
+    a, w = _fp8(a), _fp8(w)
+    _need(not a.lead and not w.lead and a.K == w.K and a.dev == w.dev,
+          "a and w: 2-D operands with the same K on one GPU")
+    _need(a.block_rows == 1, "a: must have block_rows 1")
+    _need(w.rows % 2 == 0, "w: an even number of rows, the gate's and the up projection's")
+    if _here(stream, a.dev):
+        return _fp8_gated_gemm(a, w, _act(act), out_dtype, h, gate_up)
+    with _there(stream, a.dev):
+        return _fp8_gated_gemm(a, w, _act(act), out_dtype, h, gate_up)
+
+
+def _fp8_gated_gemm(a, w, act: int, out_dtype: str, h, gate_up):
+    F = w.rows // 2
+    h, code, ld = _fp8_out(h, (a.rows, F), out_dtype, False, a[0], a.dev)
+    kept, ld2 = _gate_up(gate_up, a.rows, F, h, a.dev)
+    st = nvfp4_fp8_gated_gemm_raw(a.rows, F, a.K, a[0].data_ptr(), a[1].data_ptr(), w[0].data_ptr(),
+                                  w[1].data_ptr(), w.block_rows, act, h.data_ptr(), code, ld, _ptr(kept), ld2,
+                                  _stream(None, a.dev))
+    if st != NVFP4_OK:
+        _check("nvfp4_fp8_gated_gemm", st)
+    return h if kept is None else (h, kept)
+
+
+def nvfp4_fp8_grouped_gated_gemm(m_offsets: torch.Tensor, total_m: int, a, w, act: str = "silu",
+                                 out_dtype: str = "bf16", h: torch.Tensor | None = None, gate_up=None,
+                                 stream=None, row_index: torch.Tensor | None = None):
+    """nvfp4_fp8_gated_gemm of experts: m_offsets int32 [G+1] (GPU), a =
+    Fp8Packed [total_m, K] (or with row_index [a_rows, K]), w = Fp8Packed
+    [G, 2F, K] with block_rows 128 -> h [total_m, F], or (h, gate_up).  Rows of
+    no group stay as they were."""
+    a, w = _fp8(a), _fp8(w)
+    _need(len(w.lead) == 1 and not a.lead and a.K == w.K and a.dev == w.dev,
+          "w: [G, 2F, K] experts and a: [rows, K] with the same K, on one GPU")
+    _need(a.block_rows == 1, "a: must have block_rows 1")
+    _need(w.rows % 2 == 0, "w: an even number of rows, the gate's and the up projection's")
+    _need(w[1].shape[-1] == -(-w.rows // 128), "w: must have block_rows 128")
+    _need(row_index is not None or a.rows == total_m, "a: total_m rows (or give row_index)")
+    dev, F, code_act = w.dev, w.rows // 2, _act(act)
+    G = _groups(m_offsets, dev, w.lead[0])
+    _row_index(row_index, total_m, dev)
+    with contextlib.nullcontext() if _here(stream, dev) else _there(stream, dev):
+        h, code, ld = _fp8_out(h, (total_m, F), out_dtype, False, w[0], dev)
+        kept, ld2 = _gate_up(gate_up, total_m, F, h, dev)
+        st = nvfp4_fp8_grouped_gated_gemm_raw(G, _ptr(m_offsets), _ptr(row_index), total_m, a.rows, F, w.K,
+                                              _ptr(a[0]), _ptr(a[1]), _ptr(w[0]), _ptr(w[1]), code_act, _ptr(h),
+                                              code, ld, _ptr(kept), ld2, _stream(None, dev))
+    _check("nvfp4_fp8_grouped_gated_gemm", st)
+    return h if kept is None else (h, kept)
+
+
+def _gated_inputs(dh, gate_up):
+    _need(dh.dim() == 2 and dh.dtype in _DT_IN and dh.is_cuda, "dh: 2-D fp32 or bf16 on a GPU")
+    rows, F = dh.shape
+    _need(F % 8 == 0, "dh: columns must be a multiple of 8")
+    _need(gate_up.dtype in _DT_IN and tuple(gate_up.shape) == (rows, 2 * F),
+          f"gate_up: expected fp32 or bf16 ({rows}, {2 * F})")
+    dev = dh.get_device()
+    _on_dev(gate_up, dev, "gate_up")
+    return rows, F, _stride(dh, F, "dh"), _stride(gate_up, 2 * F, "gate_up"), dev
+
+
+def nvfp4_fp8_gated_backward(dh: torch.Tensor, gate_up: torch.Tensor, act: str = "silu", layout: str = "both",
+                             out=None, stream=None):
+    """Backward of h = act(g) * u: dh [M, F] and the kept products gate_up =
+    [g, u] [M, 2F], fp32 or bf16 each -> [dg, du] as FP8 operands with 1 x 128
+    blocks: layout "rows" (q [M, 2F], for dx = [dg, du] . W with W's "cols"
+    layout), "cols" (q [2F, M rounded up to 16], for dW = [dg, du]^T . x) or
+    "both" as a pair.  ``out`` reuses buffers."""
+    rows, F, ld_dh, ld_gu, dev = _gated_inputs(dh, gate_up)
+    code = _act(act)
+    with contextlib.nullcontext() if _here(stream, dev) else _there(stream, dev):
+        out_r, out_c = _fp8_outs(layout, out)
+        r = c = None
+        if layout != "cols":
+            r = _fp8_buffer(out_r, (rows, 2 * F), (-(-2 * F // 128), rows), 1, dh, dev)
+        if layout != "rows":
+            rows_t = -(-rows // 16) * 16
+            c = _fp8_buffer(out_c, (2 * F, rows_t), (-(-rows_t // 128), 2 * F), 1, dh, dev)
+        st = nvfp4_fp8_gated_backward_raw(_ptr(dh), _DT_IN[dh.dtype], ld_dh, _ptr(gate_up),
+                                          _DT_IN[gate_up.dtype], ld_gu, code, rows, F, *_fp8_ptrs(r, c),
+                                          _stream(None, dev))
+    _check("nvfp4_fp8_gated_backward", st)
+    return _fp8_result(r, c)
+
+
+def nvfp4_fp8_grouped_gated_backward(dh: torch.Tensor, gate_up: torch.Tensor, m_offsets: torch.Tensor,
+                                     act: str = "silu", layout: str = "both", out=None, stream=None):
+    """nvfp4_fp8_gated_backward of rows sorted by group (m_offsets int32 [G+1],
+    GPU): layouts as nvfp4_fp8_grouped_quantize's for 2F columns, "rows" for
+    nvfp4_fp8_grouped_gemm and "cols" for nvfp4_fp8_grouped_wgrad."""
+    total, F, ld_dh, ld_gu, dev = _gated_inputs(dh, gate_up)
+    code, G = _act(act), _groups(m_offsets, dev)
+    _need(G > 0 or total == 0, "m_offsets: no groups for the rows")
+    P = nvfp4_fp8_grouped_columns(total, G)
+    with contextlib.nullcontext() if _here(stream, dev) else _there(stream, dev):
+        out_r, out_c = _fp8_outs(layout, out)
+        r = c = None
+        if layout != "cols":
+            r = _fp8_buffer(out_r, (total, 2 * F), (-(-2 * F // 128), total), 1, dh, dev)
+        if layout != "rows":
+            c = _fp8_buffer(out_c, (2 * F, P), (P // 128, 2 * F), 1, dh, dev)
+        st = nvfp4_fp8_grouped_gated_backward_raw(G, _ptr(m_offsets), _ptr(dh), _DT_IN[dh.dtype], ld_dh,
+                                                  _ptr(gate_up), _DT_IN[gate_up.dtype], ld_gu, code, total, F,
+                                                  *_fp8_ptrs(r, c), _stream(None, dev))
+    _check("nvfp4_fp8_grouped_gated_backward", st)
+    return _fp8_result(r, c)
+
+
+# --------------------------------------------------------------------------
+# INT8 operands (8-bit integers, one fp32 scale per row)
+# --------------------------------------------------------------------------
+
+class Int8Packed(tuple):
+    """(q, s) of an INT8 operand [rows, K]: int8 q and fp32 s [rows], both
+    contiguous, on one GPU.  Checked when made; nvfp4_int8_quantize returns
+    one."""
+
+    def __new__(cls, ts, _trusted=None):
+        q, s = ts
+        self = super().__new__(cls, (q, s))
+        if _trusted is not None:
+            self.rows, self.K, self.dev = _trusted
+            return self
+        _need(q.dtype == torch.int8 and s.dtype == torch.float32, "q must be int8 and s fp32")
+        shape = tuple(q.shape)
+        _need(len(shape) == 2 and shape[1] % 16 == 0 and tuple(s.shape) == shape[:1],
+              f"q {shape} and s {tuple(s.shape)} do not belong together (q [rows, K] with K % 16 == 0, s [rows])")
+        _need(q.is_contiguous() and s.is_contiguous(), "q and s must be contiguous")
+        dev = q.get_device()
+        _need(q.is_cuda and s.get_device() == dev, "q and s must be on one GPU")
+        self.rows, self.K, self.dev = *shape, dev
+        return self
+
+
+def _int8(t2) -> Int8Packed:
+    return t2 if type(t2) is Int8Packed else Int8Packed(t2)
+
+
+def nvfp4_int8_quantize_raw(x, x_dtype, rows, cols, ld_x, q, s, stream=None) -> int:
+    return load().nvfp4_int8_quantize(x, x_dtype, rows, cols, ld_x, q, s, _stream(stream))
+
+
+def nvfp4_int8_gemm_raw(M, N, K, a_q, a_s, b_q, b_s, y, y_dtype, ld_y, stream=None) -> int:
+    return load().nvfp4_int8_gemm(M, N, K, a_q, a_s, b_q, b_s, y, y_dtype, ld_y, _stream(stream))
+
+
+def nvfp4_int8_quantize(x: torch.Tensor, out=None, stream=None) -> Int8Packed:
+    """x [rows, cols], fp32/bf16 on the GPU (cols % 16 == 0) -> Int8Packed with a
+    scale per row: of activations a scale per token, of a weight [N, K] one per
+    output channel.  ``out`` reuses buffers."""
+    dt = _DT_IN.get(x.dtype)
+    _need(dt is not None and x.dim() == 2, "x: 2-D fp32 or bf16")
+    _need(x.is_cuda, "x: must be on a GPU")
+    _need(x.shape[1] % 16 == 0, "x: columns must be a multiple of 16")
+    dev = x.get_device()
+    if _here(stream, dev):
+        return _int8_quantize(x, dt, out, dev)
+    with _there(stream, dev):
+        return _int8_quantize(x, dt, out, dev)
+
+
+def _int8_quantize(x, dt: int, out, dev: int) -> Int8Packed:
+    rows, cols = x.shape
+    ld = _stride(x, cols, "x")
+    if out is None:
+        out = Int8Packed((x.new_empty((rows, cols), dtype=torch.int8), x.new_empty(rows, dtype=torch.float32)),
+                         _trusted=(rows, cols, dev))
+    else:
+        out = _int8(out)
+        if (out.rows, out.K, out.dev) != (rows, cols, dev):
+            raise ValueError(f"out: expected q ({rows}, {cols}) and s ({rows},) on x's GPU")
+    st = nvfp4_int8_quantize_raw(x.data_ptr(), dt, rows, cols, ld, out[0].data_ptr(), out[1].data_ptr(),
+                                 _stream(None, dev))
+    if st != NVFP4_OK:
+        _check("nvfp4_int8_quantize", st)
+    return out
+
+
+def nvfp4_int8_gemm(a, b, out_dtype: str = "bf16", y: torch.Tensor | None = None, stream=None):
+    """a = Int8Packed [M, K], b = Int8Packed [N, K] -> y [M, N] = a . b^T in fp32
+    or bf16; the sums are exact integers.  ``y`` reuses a buffer."""
+    a, b = _int8(a), _int8(b)
+    _need(a.K == b.K and a.dev == b.dev, "a and b: operands with the same K on one GPU")
+    if _here(stream, a.dev):
+        return _int8_gemm(a, b, out_dtype, y)
+    with _there(stream, a.dev):
+        return _int8_gemm(a, b, out_dtype, y)
+
+
+def _int8_gemm(a, b, out_dtype: str, y):
+    y, code, ld = _fp8_out(y, (a.rows, b.rows), out_dtype, False, a[0], a.dev)
+    st = nvfp4_int8_gemm_raw(a.rows, b.rows, a.K, a[0].data_ptr(), a[1].data_ptr(), b[0].data_ptr(),
+                             b[1].data_ptr(), y.data_ptr(), code, ld, _stream(None, a.dev))
+    if st != NVFP4_OK:
+        _check("nvfp4_int8_gemm", st)
+    return y
+
+
+# --------------------------------------------------------------------------
+# gradient norm and clipping over a list of tensors
+# --------------------------------------------------------------------------
+
+def nvfp4_grad_workspace_bytes(count: int) -> int:
+    return int(load().nvfp4_grad_workspace_bytes(count))
+
+
+def nvfp4_grad_norm_sq_raw(count, grads, norm_sq, workspace, workspace_bytes, stream=None) -> int:
+    return load().nvfp4_grad_norm_sq(count, grads, norm_sq, workspace, workspace_bytes, _stream(stream))
+
+
+def nvfp4_clip_grads_raw(count, grads, max_norm, norm_sq, norm, workspace, workspace_bytes, stream=None) -> int:
+    return load().nvfp4_clip_grads(count, grads, max_norm, norm_sq, norm, workspace, workspace_bytes,
+                                   _stream(stream))
+
+
+def _grad_types(ts, dev: int, what: str):
+    types = [_DT_IN.get(t.dtype) for t in ts]
+    _need(None not in types and set(map(torch.Tensor.get_device, ts)) == {dev}
+          and all(map(torch.Tensor.is_contiguous, ts)), f"{what}: contiguous fp32 or bf16 tensors on one GPU")
+    return types
+
+
+def _grad_list(grads, out):
+    """The list as an array of nvfp4_grad (four 64-bit words each: g, out, n and
+    the two types), its length and its GPU.  Whole passes over the list, since a
+    model has hundreds of tensors and a Python step for each would cost more
+    than the kernels."""
+    dev = grads[0].get_device()
+    _need(dev >= 0, "grads: must be on a GPU")
+    types, sizes = _grad_types(grads, dev, "grads"), array.array("q", map(torch.Tensor.numel, grads))
+    words = array.array("q", bytes(32 * len(sizes)))
+    words[0::4] = array.array("q", map(torch.Tensor.data_ptr, grads))
+    words[2::4] = sizes
+    if out is not None:
+        out_types = _grad_types(out, dev, "out")
+        _need(array.array("q", map(torch.Tensor.numel, out)) == sizes, "out: must have the gradients' sizes")
+        words[1::4] = array.array("q", map(torch.Tensor.data_ptr, out))
+    else:
+        out_types = types
+    words[3::4] = array.array("q", [a | b << 32 for a, b in zip(types, out_types)])
+    return words, len(sizes), dev
+
+
+def _grad_workspace(workspace, count: int, like, dev: int):
+    need = nvfp4_grad_workspace_bytes(count)
+    if workspace is None:
+        return like.new_empty(need // 8, dtype=torch.float64), need
+    _on_dev(workspace, dev, "workspace")
+    _need(workspace.is_contiguous(), "workspace: must be contiguous")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def nvfp4_grad_norm_sq(grads, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Sum of the squares of all elements of a list of gradients (contiguous,
+    fp32 or bf16, one GPU) -> fp64 [1].  Where gradients are spread over
+    processes, all-reduce it and give the sum to nvfp4_clip_grads."""
+    _need(len(grads) > 0, "grads: at least one tensor")
+    words, count, dev = _grad_list(grads, None)
+    with contextlib.nullcontext() if _here(stream, dev) else _there(stream, dev):
+        ws, ws_bytes = _grad_workspace(workspace, count, grads[0], dev)
+        n2 = grads[0].new_empty(1, dtype=torch.float64)
+        st = nvfp4_grad_norm_sq_raw(count, words.buffer_info()[0], n2.data_ptr(), ws.data_ptr(), ws_bytes,
+                                    _stream(None, dev))
+    _check("nvfp4_grad_norm_sq", st)
+    return n2
+
+
+def nvfp4_clip_grads(grads, max_norm: float, norm_sq: torch.Tensor | None = None, out=None,
+                     workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Scales a list of gradients (contiguous, fp32 or bf16, one GPU) so that
+    their common norm is at most max_norm, in place or into the list ``out``
+    (fp32 or bf16), and returns the norm before that, fp32 [1].  ``norm_sq``
+    (fp64 [1], GPU): the squared norm, where it is known already.  A norm that
+    is not finite leaves the values as they are."""
+    _need(len(grads) > 0, "grads: at least one tensor")
+    _need(out is None or len(out) == len(grads), "out: one tensor per gradient")
+    _need(max_norm >= 0, "max_norm: must be at least 0")
+    words, count, dev = _grad_list(grads, out)
+    if norm_sq is not None:
+        _need(norm_sq.dtype == torch.float64 and norm_sq.numel() == 1, "norm_sq: one fp64 value")
+        _on_dev(norm_sq, dev, "norm_sq")
+    with contextlib.nullcontext() if _here(stream, dev) else _there(stream, dev):
+        ws, ws_bytes = (None, 0) if norm_sq is not None else _grad_workspace(workspace, count, grads[0], dev)
+        norm = grads[0].new_empty(1, dtype=torch.float32)
+        st = nvfp4_clip_grads_raw(count, words.buffer_info()[0], max_norm, _ptr(norm_sq), norm.data_ptr(),
+                                  _ptr(ws), ws_bytes, _stream(None, dev))
+    if st != NVFP4_OK:
+        _check("nvfp4_clip_grads", st)
+    return norm

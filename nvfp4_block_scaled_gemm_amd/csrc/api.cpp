@@ -5,6 +5,10 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+#include <memory>
+#include <new>
+
 #include "nvfp4_dispatch.h"
 #include "nvfp4_internal.h"
 
@@ -149,6 +153,100 @@ int fp8_operands_check(const uint8_t* a_q, const float* a_s, const uint8_t* b_q,
   return aligned(a_q, 16) && aligned(b_q, 16) && aligned(a_s, 4) && aligned(b_s, 4)
              ? NVFP4_OK
              : NVFP4_ERR_UNSUPPORTED;
+}
+
+// ---- gated blocks -----------------------------------------------------------
+
+constexpr int64_t kMaxGated = (int64_t)1 << 27;  // a row of 2F scales stays below 2^31 bytes
+
+bool act_ok(int act) { return act == NVFP4_SILU || act == NVFP4_GELU; }
+
+// Outputs of a gated product.
+int gated_out_check(const void* h, int h_dtype, int64_t ld_h, const void* gate_up, int64_t ld_gu,
+                    int64_t F) {
+  const int v = fp8_out_check(h, h_dtype, F, ld_h, 0);
+  if (v != NVFP4_OK || gate_up == nullptr) return v;
+  if (ld_gu < 2 * F) return NVFP4_ERR_INVALID_ARG;
+  return ld_gu > (kMaxDim << 1) || !aligned(gate_up, 2) ? NVFP4_ERR_UNSUPPORTED : NVFP4_OK;
+}
+
+nvfp4::GatedOutput gated_out(void* h, int h_dtype, int64_t ld_h, void* gate_up, int64_t ld_gu,
+                             int64_t F, int act) {
+  const bool vec2 = aligned(gate_up, 16) && ld_gu % 8 == 0 && F % 8 == 0;
+  return {fp8_out(h, h_dtype, ld_h, 0), gate_up, ld_gu, F, vec2, act};
+}
+
+// Checks both backward calls share; NVFP4_OK, an error, or 1: nothing to do.
+int gated_backward_check(const nvfp4::GatedGradient& g, int64_t rows, const uint8_t* q,
+                         const float* s, const uint8_t* qt, const float* st) {
+  if (rows < 0 || g.F < 0 || g.F % 8 != 0) return NVFP4_ERR_INVALID_ARG;
+  if (!dtype_ok(g.dh_dtype) || !dtype_ok(g.gu_dtype) || !act_ok(g.act)) return NVFP4_ERR_INVALID_ARG;
+  if (rows > kMaxDim || g.F > kMaxGated || g.ld_dh > (kMaxDim << 1) || g.ld_gu > (kMaxDim << 1))
+    return NVFP4_ERR_UNSUPPORTED;
+  if (rows == 0 || g.F == 0) return 1;
+  if (g.dh == nullptr || g.gate_up == nullptr || g.ld_dh < g.F || g.ld_gu < 2 * g.F)
+    return NVFP4_ERR_INVALID_ARG;
+  if ((q == nullptr) != (s == nullptr) || (qt == nullptr) != (st == nullptr) ||
+      (q == nullptr && qt == nullptr))
+    return NVFP4_ERR_INVALID_ARG;
+  if (!aligned(g.dh, 16) || !aligned(g.gate_up, 16) || (g.ld_dh * dtype_size(g.dh_dtype)) % 16 != 0 ||
+      (g.ld_gu * dtype_size(g.gu_dtype)) % 16 != 0)
+    return NVFP4_ERR_UNSUPPORTED;
+  return aligned(q, 16) && aligned(qt, 16) && aligned(s, 4) && aligned(st, 4) ? NVFP4_OK
+                                                                             : NVFP4_ERR_UNSUPPORTED;
+}
+
+// ---- gradients --------------------------------------------------------------
+
+int grads_check(int64_t count, const nvfp4_grad* grads) {
+  if (count < 0 || (count > 0 && grads == nullptr)) return NVFP4_ERR_INVALID_ARG;
+  if (count > ((int64_t)1 << 20)) return NVFP4_ERR_UNSUPPORTED;
+  int64_t total = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    const nvfp4_grad& g = grads[i];
+    if (g.n < 0 || !dtype_ok(g.g_dtype) || (g.n > 0 && g.g == nullptr)) return NVFP4_ERR_INVALID_ARG;
+    if (g.n > ((int64_t)1 << 42) || (total += g.n) > ((int64_t)1 << 42)) return NVFP4_ERR_UNSUPPORTED;
+    if (!aligned(g.g, dtype_size(g.g_dtype))) return NVFP4_ERR_UNSUPPORTED;
+  }
+  return NVFP4_OK;
+}
+
+// Outputs: their types and alignment, and that no written tensor overlaps
+// another one (each would be scaled by whoever comes first).
+int grad_outs_check(int64_t count, const nvfp4_grad* grads) {
+  struct Range {
+    uintptr_t begin, end;
+    bool written;
+  };
+  Range few[256];
+  std::unique_ptr<Range[]> many;
+  if (count > 128) many.reset(new (std::nothrow) Range[2 * count]);
+  if (count > 128 && many == nullptr) return NVFP4_ERR_UNSUPPORTED;
+  Range* r = count > 128 ? many.get() : few;
+  int64_t n = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    const nvfp4_grad& g = grads[i];
+    const bool in_place = g.out == nullptr || g.out == g.g;
+    if (!dtype_ok(g.out_dtype) || (in_place && g.out_dtype != g.g_dtype)) return NVFP4_ERR_INVALID_ARG;
+    if (!aligned(g.out, dtype_size(g.out_dtype))) return NVFP4_ERR_UNSUPPORTED;
+    if (g.n == 0) continue;
+    const uintptr_t a = (uintptr_t)g.g, b = (uintptr_t)g.out;
+    r[n++] = {a, a + (uintptr_t)(g.n * dtype_size(g.g_dtype)), in_place};
+    if (!in_place) r[n++] = {b, b + (uintptr_t)(g.n * dtype_size(g.out_dtype)), true};
+  }
+  std::sort(r, r + n, [](const Range& x, const Range& y) { return x.begin < y.begin; });
+  uintptr_t read_to = 0, written_to = 0;  // ends of what starts before
+  for (int64_t i = 0; i < n; ++i) {
+    if (r[i].begin < written_to || (r[i].written && r[i].begin < read_to)) return NVFP4_ERR_INVALID_ARG;
+    uintptr_t& to = r[i].written ? written_to : read_to;
+    to = std::max(to, r[i].end);
+  }
+  return NVFP4_OK;
+}
+
+int grad_workspace_check(int64_t count, const void* workspace, size_t bytes) {
+  if (workspace == nullptr || bytes < nvfp4::grad_workspace_bytes(count)) return NVFP4_ERR_INVALID_ARG;
+  return aligned(workspace, 8) ? NVFP4_OK : NVFP4_ERR_UNSUPPORTED;
 }
 
 // Checks both router calls share.
@@ -439,6 +537,122 @@ int nvfp4_fp8_grouped_wgrad(int32_t G, const int32_t* m_offsets, int64_t total_m
   return from_fp8(nvfp4::launch_fp8_wgrad(G, m_offsets, total_m, P, N, K, {a_q, a_s}, {b_q, b_s},
                                           fp8_out(dw, (int)dw_dtype, K, flags),
                                           (hipStream_t)stream));
+}
+
+int nvfp4_fp8_gated_gemm(int64_t M, int64_t F, int64_t K, const uint8_t* a_q, const float* a_s,
+                         const uint8_t* w_q, const float* w_s, int w_block_rows, nvfp4_act act,
+                         void* h, nvfp4_dtype h_dtype, int64_t ld_h, void* gate_up,
+                         int64_t ld_gate_up, void* stream) {
+  if (M < 0 || F < 0 || K < 0 || K % 16 != 0) return NVFP4_ERR_INVALID_ARG;
+  if ((w_block_rows != 1 && w_block_rows != 128) || !act_ok((int)act)) return NVFP4_ERR_INVALID_ARG;
+  if (M > kMaxDim || F > kMaxGated || K > kMaxFp8K) return NVFP4_ERR_UNSUPPORTED;
+  if (M == 0 || F == 0) return NVFP4_OK;
+  int v = gated_out_check(h, (int)h_dtype, ld_h, gate_up, ld_gate_up, F);
+  if (v == NVFP4_OK && K > 0) v = fp8_operands_check(a_q, a_s, w_q, w_s);
+  if (v != NVFP4_OK) return v;
+  return from_fp8(nvfp4::launch_fp8_gated(
+      M, F, K, {a_q, a_s}, {w_q, w_s}, w_block_rows,
+      gated_out(h, (int)h_dtype, ld_h, gate_up, ld_gate_up, F, (int)act), (hipStream_t)stream));
+}
+
+int nvfp4_fp8_grouped_gated_gemm(int32_t G, const int32_t* m_offsets, const int32_t* row_index,
+                                 int64_t total_m, int64_t a_rows, int64_t F, int64_t K,
+                                 const uint8_t* a_q, const float* a_s, const uint8_t* w_q,
+                                 const float* w_s, nvfp4_act act, void* h, nvfp4_dtype h_dtype,
+                                 int64_t ld_h, void* gate_up, int64_t ld_gate_up, void* stream) {
+  if (G < 0 || total_m < 0 || F < 0 || K < 0 || K % 16 != 0) return NVFP4_ERR_INVALID_ARG;
+  if ((G == 0 && total_m != 0) || a_rows < 0 || !act_ok((int)act)) return NVFP4_ERR_INVALID_ARG;
+  if (row_index == nullptr && a_rows != 0 && a_rows != total_m) return NVFP4_ERR_INVALID_ARG;
+  if (total_m > kMaxDim || a_rows > kMaxDim || F > kMaxGated || K > kMaxFp8K)
+    return NVFP4_ERR_UNSUPPORTED;
+  if (total_m == 0 || F == 0) return NVFP4_OK;
+  if (m_offsets == nullptr) return NVFP4_ERR_INVALID_ARG;
+  int v = gated_out_check(h, (int)h_dtype, ld_h, gate_up, ld_gate_up, F);
+  if (v == NVFP4_OK && K > 0) v = fp8_operands_check(a_q, a_s, w_q, w_s);
+  if (v != NVFP4_OK) return v;
+  if (row_index != nullptr && a_rows * K >= ((int64_t)1 << 31)) return NVFP4_ERR_UNSUPPORTED;
+  return from_fp8(nvfp4::launch_fp8_grouped_gated(
+      G, m_offsets, row_index, total_m, a_rows, F, K, {a_q, a_s}, {w_q, w_s},
+      gated_out(h, (int)h_dtype, ld_h, gate_up, ld_gate_up, F, (int)act), (hipStream_t)stream));
+}
+
+int nvfp4_fp8_gated_backward(const void* dh, nvfp4_dtype dh_dtype, int64_t ld_dh,
+                             const void* gate_up, nvfp4_dtype gate_up_dtype, int64_t ld_gate_up,
+                             nvfp4_act act, int64_t rows, int64_t F, uint8_t* q, float* s,
+                             uint8_t* qt, float* st, void* stream) {
+  const nvfp4::GatedGradient g{dh, gate_up, ld_dh, ld_gate_up, F, (int)dh_dtype, (int)gate_up_dtype, (int)act};
+  const int v = gated_backward_check(g, rows, q, s, qt, st);
+  if (v != NVFP4_OK) return v == 1 ? NVFP4_OK : v;
+  return from_fp8(nvfp4::launch_fp8_gated_backward(g, rows, q, s, qt, st, (hipStream_t)stream));
+}
+
+int nvfp4_fp8_grouped_gated_backward(int32_t G, const int32_t* m_offsets, const void* dh,
+                                     nvfp4_dtype dh_dtype, int64_t ld_dh, const void* gate_up,
+                                     nvfp4_dtype gate_up_dtype, int64_t ld_gate_up, nvfp4_act act,
+                                     int64_t total_m, int64_t F, uint8_t* q, float* s, uint8_t* qt,
+                                     float* st, void* stream) {
+  if (G < 0 || (G == 0 && total_m != 0)) return NVFP4_ERR_INVALID_ARG;
+  const nvfp4::GatedGradient g{dh, gate_up, ld_dh, ld_gate_up, F, (int)dh_dtype, (int)gate_up_dtype, (int)act};
+  const int v = gated_backward_check(g, total_m, q, s, qt, st);
+  if (v != NVFP4_OK) return v == 1 ? NVFP4_OK : v;
+  if (m_offsets == nullptr) return NVFP4_ERR_INVALID_ARG;
+  return from_fp8(nvfp4::launch_fp8_grouped_gated_backward(g, G, m_offsets, total_m, q, s, qt, st,
+                                                           (hipStream_t)stream));
+}
+
+int nvfp4_int8_quantize(const void* x, nvfp4_dtype x_dtype, int64_t rows, int64_t cols,
+                        int64_t ld_x, int8_t* q, float* s, void* stream) {
+  // the FP8 quantiser's checks of one layout
+  const int v = fp8_quantize_check(x, (int)x_dtype, rows, cols, ld_x, reinterpret_cast<const uint8_t*>(q), s,
+                                   nullptr, nullptr);
+  if (v != NVFP4_OK) return v == 1 ? NVFP4_OK : v;
+  return from_fp8(nvfp4::launch_int8_quantize(x, (int)x_dtype, rows, cols, ld_x, q, s, (hipStream_t)stream));
+}
+
+int nvfp4_int8_gemm(int64_t M, int64_t N, int64_t K, const int8_t* a_q, const float* a_s,
+                    const int8_t* b_q, const float* b_s, void* y, nvfp4_dtype y_dtype,
+                    int64_t ld_y, void* stream) {
+  if (M < 0 || N < 0 || K < 0 || K % 16 != 0) return NVFP4_ERR_INVALID_ARG;
+  if (M > kMaxDim || N > kMaxDim || K >= ((int64_t)1 << 17)) return NVFP4_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return NVFP4_OK;
+  int v = fp8_out_check(y, (int)y_dtype, N, ld_y, 0);
+  if (v != NVFP4_OK) return v;
+  // the scales are read for K == 0 too
+  if (a_s == nullptr || b_s == nullptr || (K > 0 && (a_q == nullptr || b_q == nullptr)))
+    return NVFP4_ERR_INVALID_ARG;
+  if (!aligned(a_q, 16) || !aligned(b_q, 16) || !aligned(a_s, 4) || !aligned(b_s, 4))
+    return NVFP4_ERR_UNSUPPORTED;
+  return from_fp8(nvfp4::launch_int8_gemm(M, N, K, {a_q, a_s}, {b_q, b_s},
+                                          fp8_out(y, (int)y_dtype, ld_y, 0), (hipStream_t)stream));
+}
+
+size_t nvfp4_grad_workspace_bytes(int64_t count) {
+  return count < 0 ? 0 : nvfp4::grad_workspace_bytes(count);
+}
+
+int nvfp4_grad_norm_sq(int64_t count, const nvfp4_grad* grads, double* norm_sq, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  int v = grads_check(count, grads);
+  if (v != NVFP4_OK) return v;
+  if (norm_sq == nullptr) return NVFP4_ERR_INVALID_ARG;
+  v = grad_workspace_check(count, workspace, workspace_bytes);
+  if (v != NVFP4_OK) return v;
+  if (!aligned(norm_sq, 8)) return NVFP4_ERR_UNSUPPORTED;
+  return from_hip(nvfp4::launch_grad_norm_sq(count, grads, norm_sq, (double*)workspace, (hipStream_t)stream));
+}
+
+int nvfp4_clip_grads(int64_t count, const nvfp4_grad* grads, double max_norm,
+                     const double* norm_sq, float* norm, void* workspace, size_t workspace_bytes,
+                     void* stream) {
+  int v = grads_check(count, grads);
+  if (v == NVFP4_OK) v = grad_outs_check(count, grads);
+  if (v != NVFP4_OK) return v;
+  if (!(max_norm >= 0)) return NVFP4_ERR_INVALID_ARG;
+  if (norm_sq == nullptr) v = grad_workspace_check(count, workspace, workspace_bytes);
+  if (v != NVFP4_OK) return v;
+  if (!aligned(norm_sq, 8) || !aligned(norm, 4)) return NVFP4_ERR_UNSUPPORTED;
+  return from_hip(nvfp4::launch_clip_grads(count, grads, max_norm, norm_sq, norm, (double*)workspace,
+                                           (hipStream_t)stream));
 }
 
 size_t nvfp4_moe_route_workspace_bytes(int64_t T, int64_t E) {

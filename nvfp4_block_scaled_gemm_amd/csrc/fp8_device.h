@@ -99,6 +99,15 @@ __device__ __forceinline__ f32x4 mfma_block(const F16Block& a, const F16Block& b
   return c;
 }
 
+// The same block in 8-bit integers, one half of it (64 elements) added to 32-bit
+// sums: half h is the lane's chunk h of 16 bytes in both operands.
+template <int H>
+__device__ __forceinline__ i32x4 mfma_half(const i32x8& a, const i32x8& b, const i32x4& c) {
+  const i32x4 x = __builtin_shufflevector(a, a, 4 * H, 4 * H + 1, 4 * H + 2, 4 * H + 3);
+  const i32x4 y = __builtin_shufflevector(b, b, 4 * H, 4 * H + 1, 4 * H + 2, 4 * H + 3);
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(x, y, c, 0, 0, 0);
+}
+
 // A fragment as the matrix instructions take it.
 template <bool WIDE>
 __device__ __forceinline__ auto fragment(const i32x8& w) {

@@ -26,9 +26,20 @@
 //  * Rows past the operand read as zeros by the descriptors' range; a last
 //    block shorter than 128 reads zeros past K in both operands (K % 16 == 0,
 //    so a 16-byte chunk is wholly inside or outside).
+//
+// Two other products run in the same tile:
+//  * GATED, a gated block's: the weight rows are taken 32 of the gate, 32 of
+//    the up projection in turn, so a wave's 64 rows give both factors of 32
+//    outputs in the same lane, and the epilogue writes act(gate) * up (and the
+//    two products, if they are kept).  The main loop differs in the two weight
+//    scales alone.
+//  * INT8, with one scale for each row of either operand: the sums are 32-bit
+//    integers that stay in the accumulators to the end, the scales are applied
+//    as the tile goes out, and a stage holds no scales.
 #pragma once
 
 #include "fp8_device.h"
+#include "gated_act.h"
 
 namespace nvfp4 {
 namespace fp8 {
@@ -44,6 +55,12 @@ struct TileOperand {
   const int32_t* index;  // gathered rows (nullptr: rows in order)
   int32_t index_n;       // rows of the tile
   int32_t index_max;     // rows of the operand
+  // gated weights: q points at the tile's first gate row, s at block 0 of the
+  // whole weight's scales
+  int64_t up_q = 0;       // bytes from a gate row to its up row
+  int64_t row0 = 0;       // the tile's first gate row
+  int64_t up = 0;         // rows from a gate row to its up row
+  int shift = 0;          // rows per scale, as a power of two
 };
 
 struct TileOut {
@@ -53,6 +70,12 @@ struct TileOut {
   int dtype;      // 0 fp32, 1 bf16
   bool add;       // fp32: y += product
   bool vec;       // rows are 16-byte aligned
+  // gated: where the two products go in bf16 (nullptr: nowhere)
+  void* gate = nullptr;
+  void* upto = nullptr;
+  int64_t ld2 = 0;
+  bool vec2 = false;
+  int act = kSilu;
 };
 
   // Eight neighbouring outputs of one row (those below out.n).
@@ -94,17 +117,18 @@ struct TileOut {
 // ring of its own, and add their sums at the end (in group order): small
 // tiles spend a step mostly on meeting and on LDS latency, so fewer steps with
 // two waves on each SIMD pay.
-template <int BM, int BN, int WM, int WN, int STAGES, int KG, bool BROWS, bool WIDE>
+template <int BM, int BN, int WM, int WN, int STAGES, int KG, bool BROWS, bool WIDE,
+          bool GATED = false, bool INT8 = false>
 struct Tile {
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves * KG;
   static constexpr int TM = BM / WM, TN = BN / WN;
   static constexpr int FM = TM / 16, FN = TN / 16;
   static constexpr int kALoads = BM / 8 / kWaves, kBLoads = BN / 8 / kWaves;
-  static constexpr int kScales = (BM + BN) / 64;  // scale-load instructions of a stage
+  static constexpr int kScales = INT8 ? 0 : (BM + BN) / 64;  // scale-load instructions of a stage
   static constexpr int kSLoads = (kScales + kWaves - 1) / kWaves;
   static constexpr int kLoads = kALoads + kBLoads + kSLoads;  // per wave and stage
   static constexpr int kAOff = 0, kBOff = BM * kBlock, kSOff = (BM + BN) * kBlock;
-  static constexpr int kStage = kSOff + (BM + BN) * 4;
+  static constexpr int kStage = kSOff + (INT8 ? 0 : (BM + BN) * 4);
   static constexpr int kSmem = KG * STAGES * kStage;
   static_assert((KG - 1) * BM * BN * 4 <= kSmem, "the groups' sums fit the rings");
   static_assert(BM % (8 * kWaves) == 0 && BN % (8 * kWaves) == 0, "whole loads per wave");
@@ -114,6 +138,9 @@ struct Tile {
   static_assert(BROWS || 128 % TN == 0, "one weight scale per wave and block");
   static_assert(FM % 2 == 0 && FN >= 2, "pairs of fragments");
   static_assert((STAGES - 1) * kLoads < 64, "vmcnt range");
+  static_assert(!GATED || (TN == 64 && kBLoads <= 4), "a wave's weight loads are all of one projection");
+  static_assert(!INT8 || (!BROWS && !WIDE && !GATED), "integers have one kind of product");
+  using Acc = std::conditional_t<INT8, i32x4, f32x4>;
 
   // 16 lanes of an activation fragment read rows r .. r + 15: two rows share
   // a 256-byte bank line, so the chunk moves with row / 2.
@@ -134,12 +161,15 @@ struct Tile {
     const int li = lane & 15, lg = lane >> 4;
     const int nk = (int)((K + kBlock - 1) / kBlock), steps = (nk + KG - 1) / KG;
     // plain copies: a choice between two fields stays a choice of registers
-    const uint8_t *const aq = A.q, *const bq = B.q;
+    const uint8_t* const aq = A.q;
+    // gated: this wave loads 32 (16) rows of one of the projections
+    const bool up_wave = GATED && (wave * kBLoads * 8) % 64 >= 32;
+    const uint8_t* const bq = B.q + (GATED && up_wave ? B.up_q : 0);
     const float *const as = A.s, *const bs = B.s;
     const int64_t as_ld = A.s_ld, bs_ld = B.s_ld;
     const uint32_t aq_bytes = A.q_bytes, bq_bytes = B.q_bytes, as_bytes = A.s_bytes, bs_bytes = B.s_bytes;
 
-    uint32_t a_off[kALoads], b_off[kBLoads], s_off[kSLoads];
+    uint32_t a_off[kALoads], b_off[kBLoads], s_off[kSLoads ? kSLoads : 1];
     // a load's 16-byte chunk of its rows; rows 8 apart only flip fixed bits
     const int lr = lane >> 3;
     const uint32_t a_chunk = (uint32_t)(((lane & 7) ^ swz_a(wave * kALoads * 8 + lr)) << 4);
@@ -159,7 +189,8 @@ struct Tile {
 #pragma unroll
     for (int i = 0; i < kBLoads; ++i) {
       const int r = (wave * kBLoads + i) * 8 + (lane >> 3);
-      b_off[i] = (uint32_t)r * ld + (b_chunk ^ (swz_b(i * 8) << 4));
+      const int row = GATED ? (r >> 6) * 32 + (r & 31) : r;
+      b_off[i] = (uint32_t)row * ld + (b_chunk ^ (swz_b(i * 8) << 4));
     }
     // chunks of the last block that lie past K: lane masks in scalar
     // registers, so a stage's loads need no branch (one would let the
@@ -173,11 +204,11 @@ struct Tile {
     // scale loads: instruction j < BM / 64 takes the activations' rows, the
     // others the weights'; waves past the last repeat one (same bytes, same
     // place), so every wave issues the same number of loads
-    bool s_is_a[kSLoads];
-    int s_slot[kSLoads];
+    bool s_is_a[kSLoads ? kSLoads : 1];
+    int s_slot[kSLoads ? kSLoads : 1];
 #pragma unroll
     for (int i = 0; i < kSLoads; ++i) {
-      const int j = (wave * kSLoads + i) % kScales;
+      const int j = (wave * kSLoads + i) % (kScales ? kScales : 1);
       s_slot[i] = j;
       s_is_a[i] = j < BM / 64;
       const int r = (s_is_a[i] ? j : j - BM / 64) * 64 + lane;
@@ -190,6 +221,9 @@ struct Tile {
           row = (uint32_t)v;
         }
         s_off[i] = ok ? row * 4 : kNoRow;
+      } else if constexpr (GATED) {
+        const int64_t row = B.row0 + (r >> 6) * 32 + (r & 31) + ((r & 32) ? B.up : 0);
+        s_off[i] = (uint32_t)(row >> B.shift) * 4;
       } else {
         s_off[i] = (uint32_t)(BROWS ? r : r / kBlock) * 4;
       }
@@ -224,11 +258,11 @@ struct Tile {
       static_for<decltype(n)::value>([&](auto jc) { load_one(s, slot, jc); });
     };
 
-    f32x4 acc[FN][FM];
+    Acc acc[FN][FM];
 #pragma unroll
     for (int i = 0; i < FN; ++i)
 #pragma unroll
-      for (int j = 0; j < FM; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int j = 0; j < FM; ++j) acc[i][j] = Acc{0, 0, 0, 0};
 
     // fragments: a lane takes chunks lg and lg + 4 of its row in both
     // operands (the swizzles do not depend on the fragment's number)
@@ -258,7 +292,7 @@ struct Tile {
     using Frag = decltype(fragment<WIDE>(i32x8{}));
     constexpr int PAIRS = FM / 2, PER = 2 * FN, Q = PAIRS * PER;
     i32x8 br[FN], ar[2];
-    float fw = 1.f;
+    float fw[GATED ? 2 : 1];
     f32x4 fb[BROWS ? FN : 1];
     f32x4 cq[3];
     Frag bw[FN], aw[2];
@@ -272,7 +306,7 @@ struct Tile {
     issue(STAGES - 1, STAGES - 1, std::integral_constant<int, EARLY>{});
     wait_vmcnt<(STAGES - 2) * kLoads + EARLY>();
     workgroup_barrier();
-    if (wm * TM >= out.m || wn * TN >= out.n) {
+    if (wm * TM >= out.m || wn * (GATED ? TN / 2 : TN) >= out.n) {
       // no output of this wave exists (a group's last rows): it only loads
       // and meets the others, and leaves the matrix core to the wave beside it
       int slot = 0;
@@ -300,24 +334,31 @@ struct Tile {
       const int next = slot + 1 == STAGES ? 0 : slot + 1;
       const uint8_t* nst = smem + next * kStage;
       const float* sc = scales(st);
-      if constexpr (BROWS) {
+      // scale of a row of A times that of W's block; gated: of either projection
+      float fall[GATED && !BROWS ? 2 : 1][FM];
+      if constexpr (INT8) {
+      } else if constexpr (BROWS) {
 #pragma unroll
         for (int i = 0; i < FN; ++i)
           fb[i] = *reinterpret_cast<const f32x4*>(sc + BM + wn * TN + 32 * (i >> 1) + 8 * lg + 4 * (i & 1));
       } else {
-        fw = sc[BM + wn * TN];
+        fw[0] = sc[BM + wn * TN];
+        if constexpr (GATED) fw[1] = sc[BM + wn * TN + 32];
       }
-      float fall[FM];
+      if constexpr (!INT8) {
 #pragma unroll
-      for (int j = 0; j < FM; ++j) fall[j] = sc[a_row0 + 16 * j];
+        for (int j = 0; j < FM; ++j) fall[0][j] = sc[a_row0 + 16 * j];
+      }
       i32x8 an[2];
       auto add = [&](auto qc) {
         constexpr int q = decltype(qc)::value, p = q / PER, i = (q % PER) / 2, h = q % 2, j = 2 * p + h;
-        const f32x4& c = cq[q % 3];
+        if constexpr (!INT8) {
+          const f32x4& c = cq[q % 3];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float f = BROWS ? fb[BROWS ? i : 0][e] * fall[j] : fall[j];
-          acc[i][j][e] = __builtin_fmaf(c[e], f, acc[i][j][e]);
+          for (int e = 0; e < 4; ++e) {
+            const float f = BROWS ? fb[BROWS ? i : 0][e] * fall[0][j] : fall[GATED && !BROWS ? i >> 1 : 0][j];
+            acc[i][j][e] = __builtin_fmaf(c[e], f, acc[i][j][e]);
+          }
         }
       };
       static_for<Q>([&](auto qc) {
@@ -334,11 +375,21 @@ struct Tile {
           aw[1] = fragment<WIDE>(ar[1]);
         }
         if constexpr (p == 0 && h == 0) bw[i] = fragment<WIDE>(br[i]);
-        if constexpr (p == 0 && r == 0 && !BROWS) {
+        if constexpr (p == 0 && r == 0 && !BROWS && !INT8) {
 #pragma unroll
-          for (int j = 0; j < FM; ++j) fall[j] *= fw;
+          for (int j = 0; j < FM; ++j) {
+            if constexpr (GATED) fall[1][j] = fall[0][j] * fw[1];
+            fall[0][j] *= fw[0];
+          }
         }
-        cq[q % 3] = mfma_block(bw[i], aw[h]);
+        if constexpr (INT8) {
+          // the block's halves in turn over the pair, so that a sum is used
+          // again two instructions later
+#pragma unroll
+          for (int k = 0; k < 2; ++k) acc[i][2 * p + k] = mfma_half<h>(bw[i], aw[k], acc[i][2 * p + k]);
+        } else {
+          cq[q % 3] = mfma_block(bw[i], aw[h]);
+        }
         if constexpr (q >= 2) add(std::integral_constant<int, q - 2>{});
         if constexpr (last && r == 0) workgroup_barrier();
         // refill: load n at MEET + n * SPREAD / kLoads, counted on into the
@@ -378,7 +429,7 @@ struct Tile {
     workgroup_barrier();
     if constexpr (KG > 1) {
       // the other groups' sums, each lane's own outputs
-      f32x4* sums = reinterpret_cast<f32x4*>(smem_all) + wave * (FM * FN * 64) + lane;
+      Acc* sums = reinterpret_cast<Acc*>(smem_all) + wave * (FM * FN * 64) + lane;
       constexpr int kGroupSums = kWaves * FM * FN * 64;
       if (kg > 0) {
 #pragma unroll
@@ -399,12 +450,54 @@ struct Tile {
     constexpr int kStageAt = (KG - 1) * BM * BN;  // floats: behind the groups' sums
     static_assert((kStageAt + kWaves * 32 * RS) * 4 <= kSmem, "staging fits the ring");
     float* stage = reinterpret_cast<float*>(smem_all) + kStageAt + wave * 32 * RS;
+    if constexpr (GATED) {
+      // eight outputs a lane: their gates and, 32 columns on, their ups
+      const TileOut gate{out.gate, out.ld2, out.m, out.n, 1, false, out.vec2};
+      const TileOut up{out.upto, out.ld2, out.m, out.n, 1, false, out.vec2};
+#pragma unroll
+      for (int j2 = 0; j2 < FM / 2; ++j2) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < FN; ++i)
+            *reinterpret_cast<f32x4*>(stage + (16 * h + li) * RS + 32 * (i >> 1) + 8 * lg + 4 * (i & 1)) = acc[i][2 * j2 + h];
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const int r = p * 16 + lane / 4, c = lane % 4 * 8;
+          const int m = wm * TM + 32 * j2 + r, n = wn * 32 + c;
+          float g[8], u[8], v[8];
+          const f32x4* at = reinterpret_cast<const f32x4*>(stage + r * RS + c);
+          const f32x4 g0 = at[0], g1 = at[1], u0 = at[8], u1 = at[9];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            g[e] = g0[e];
+            g[4 + e] = g1[e];
+            u[e] = u0[e];
+            u[4 + e] = u1[e];
+          }
+          gated8(out.act, g, u, v);
+          if (m < out.m) {
+            store8(out, m, n, v);
+            if (out.gate != nullptr) {
+              store8(gate, m, n, g);
+              store8(up, m, n, u);
+            }
+          }
+        }
+      }
+      return;
+    }
     constexpr int LPR = TN / 8, RPI = 64 / LPR;  // lanes per row, rows per read
     constexpr int NP = 32 / RPI;
     // Whole aligned rows leave in 16-byte pieces, fp32 ones as two runs TN / 2
     // columns apart (what they add to is read ahead of everything, in one
     // go); other rows element by element, a lane a column.
     const bool runs = out.vec && (wn + 1) * TN <= out.n;
+    float col_scale[8];
+    if constexpr (INT8) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) col_scale[e] = B.s[min(wn * TN + 8 * (lane % LPR) + e, out.n - 1)];
+    }
     float* const y32 = reinterpret_cast<float*>(out.y) + wn * TN + 4 * (lane % LPR);
     f32x4 old[WIDE ? FM / 2 : 1][WIDE ? NP : 1][2];
     if constexpr (WIDE) {
@@ -431,8 +524,24 @@ struct Tile {
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int i = 0; i < FN; ++i)
-          *reinterpret_cast<f32x4*>(stage + (16 * h + li) * RS + 32 * (i >> 1) + 8 * lg + 4 * (i & 1)) = acc[i][2 * j2 + h];
-      if (runs) {
+          *reinterpret_cast<Acc*>(stage + (16 * h + li) * RS + 32 * (i >> 1) + 8 * lg + 4 * (i & 1)) = acc[i][2 * j2 + h];
+      if constexpr (INT8) {
+        // eight outputs a lane, each an integer times its row's and its column's scale
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+          const int r = p * RPI + lane / LPR, c = 8 * (lane % LPR);
+          const int m = wm * TM + 32 * j2 + r, n = wn * TN + c;
+          const i32x4 lo = *reinterpret_cast<const i32x4*>(stage + r * RS + c);
+          const i32x4 hi = *reinterpret_cast<const i32x4*>(stage + r * RS + c + 4);
+          if (m < out.m) {
+            const float sm = A.s[m];
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = (float)(e < 4 ? lo[e & 3] : hi[e & 3]) * sm * col_scale[e];
+            store8(out, m, n, v);
+          }
+        }
+      } else if (runs) {
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
           const int r = p * RPI + lane / LPR, c = lane % LPR;

@@ -6,6 +6,8 @@
 #include <stdint.h>
 #include <stddef.h>
 
+#include "nvfp4.h"
+
 namespace nvfp4 {
 
 // quantize.hip
@@ -167,6 +169,43 @@ hipError_t launch_fp8_wgrad(int32_t G, const int32_t* m_offsets, int64_t total_m
                             int64_t N, int64_t K, Fp8Operand a, Fp8Operand b, Fp8Out y,
                             hipStream_t stream);
 
+// fp8_gated.hip: h [M, F] = act(a Wg^T) * (a Wu^T), b = [Wg; Wu] [2F, K]; the
+// two products as well where gate_up is not null.
+struct GatedOutput {
+  Fp8Out h;
+  void* gate_up;  // bf16 [M, 2F]
+  int64_t ld2, F;
+  bool vec2;  // both halves' rows start on 16-byte borders
+  int act;    // 0 silu, 1 gelu
+};
+hipError_t launch_fp8_gated(int64_t M, int64_t F, int64_t K, Fp8Operand a, Fp8Operand b, int b_block_rows,
+                            GatedOutput y, hipStream_t stream);
+hipError_t launch_fp8_grouped_gated(int32_t G, const int32_t* m_offsets, const int32_t* row_index, int64_t total_m,
+                                    int64_t a_rows, int64_t F, int64_t K, Fp8Operand a, Fp8Operand b, GatedOutput y,
+                                    hipStream_t stream);
+// fp8_gated_backward.hip: rows layout q/s and transposed layout qt/st (either may
+// be null).
+struct GatedGradient {
+  const void* dh;       // [rows, F]
+  const void* gate_up;  // [rows, 2F]
+  int64_t ld_dh, ld_gu, F;
+  int dh_dtype, gu_dtype, act;
+};
+hipError_t launch_fp8_gated_backward(GatedGradient g, int64_t rows, uint8_t* q, float* s, uint8_t* qt, float* st,
+                                     hipStream_t stream);
+hipError_t launch_fp8_grouped_gated_backward(GatedGradient g, int32_t G, const int32_t* m_offsets, int64_t total_m,
+                                             uint8_t* q, float* s, uint8_t* qt, float* st, hipStream_t stream);
+
+// int8_quantize.hip, int8_gemm.hip: 8-bit integers [rows, K] and a scale per row.
+struct Int8Operand {
+  const int8_t* q;
+  const float* s;  // [rows]
+};
+hipError_t launch_int8_quantize(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ld_x, int8_t* q,
+                                float* s, hipStream_t stream);
+hipError_t launch_int8_gemm(int64_t M, int64_t N, int64_t K, Int8Operand a, Int8Operand b, Fp8Out y,
+                            hipStream_t stream);
+
 // moe_route.hip
 struct RouteOut {
   int32_t* expert_index;  // [T, k]
@@ -188,5 +227,13 @@ hipError_t launch_moe_route_backward(int64_t T, int64_t E, int topk, const void*
                                      const int32_t* routed, const float* d_weights,
                                      const float* d_loss, void* d_logits, int64_t ld_d,
                                      hipStream_t stream);
+
+// grad_clip.hip: lists of checked tensors (out set); norm_sq == nullptr: computed
+// from the list first; norm may be null.
+size_t grad_workspace_bytes(int64_t count);
+hipError_t launch_grad_norm_sq(int64_t count, const nvfp4_grad* grads, double* norm_sq, double* workspace,
+                               hipStream_t stream);
+hipError_t launch_clip_grads(int64_t count, const nvfp4_grad* grads, double max_norm, const double* norm_sq,
+                             float* norm, double* workspace, hipStream_t stream);
 
 }  // namespace nvfp4

@@ -17,3 +17,7 @@ from .fp8_ref import (  # noqa: F401
     fp8_grouped_quantize_t_ref, fp8_quantize_ref, fp8_quantize_t_ref, fp8_tolerance,
     moe_route_backward_ref, moe_route_ref,
 )
+from .feed_forward_ref import (  # noqa: F401
+    act_error, act_ref, clip_ref, gated_backward_ref, gated_ref, gated_tolerance, int8_gemm_ref,
+    int8_quantize_ref, sums_tolerance,
+)
