@@ -465,7 +465,8 @@ int nvfp4_fp8_grouped_gated_backward(int32_t G, const int32_t* m_offsets, const 
  * nvfp4_int8_quantize: x [rows, cols] (F32 or BF16, row stride ld_x) -> q, s.
  * Per row: A = max(max|x|, 2^-100), s = fl32(A / 127), each q is
  * fl32(x * fl32(127 / A)) rounded to the nearest integer, ties to even.  A row
- * holding a NaN or an infinity gets a NaN scale and zeros.  Deterministic.
+ * holding a NaN or an infinity gets a NaN scale and zeros; a row of no columns
+ * has the scale of a zero row.  Deterministic.
  * Errors: NVFP4_ERR_INVALID_ARG for cols % 16 != 0, negative sizes, a bad
  * dtype, ld_x < cols or a null pointer; NVFP4_ERR_UNSUPPORTED for x, its rows
  * or q not 16-byte aligned, s not 4-byte aligned, a dimension above 2^30, or
@@ -478,7 +479,7 @@ int nvfp4_int8_quantize(const void* x, nvfp4_dtype x_dtype, int64_t rows, int64_
  * y[m, n] = fl32(sum_k a_q[m, k] b_q[n, k]) * a_s[m] * b_s[n] (in this order) of
  * INT8 operands a [M, K] and b = W [N, K].  The sum is an exact 32-bit integer.
  * y [M, N] (F32 or BF16) has row stride ld_y >= N.  A NaN scale gives NaN in
- * its row (column).  K == 0 writes zeros.
+ * its row (column), for K == 0 too, whose sums are 0.
  * Errors: NVFP4_ERR_INVALID_ARG for K % 16 != 0, negative sizes, a bad dtype,
  * ld_y < N or a null pointer; NVFP4_ERR_UNSUPPORTED for q not 16-byte aligned,
  * s or y not aligned to their elements, K >= 2^17 (where a sum could pass 32

@@ -602,10 +602,15 @@ int nvfp4_fp8_grouped_gated_backward(int32_t G, const int32_t* m_offsets, const 
 
 int nvfp4_int8_quantize(const void* x, nvfp4_dtype x_dtype, int64_t rows, int64_t cols,
                         int64_t ld_x, int8_t* q, float* s, void* stream) {
-  // the FP8 quantiser's checks of one layout
-  const int v = fp8_quantize_check(x, (int)x_dtype, rows, cols, ld_x, reinterpret_cast<const uint8_t*>(q), s,
-                                   nullptr, nullptr);
-  if (v != NVFP4_OK) return v == 1 ? NVFP4_OK : v;
+  if (rows < 0 || cols < 0 || cols % 16 != 0 || !dtype_ok((int)x_dtype)) return NVFP4_ERR_INVALID_ARG;
+  if (rows > kMaxDim || cols > kMaxDim || ld_x > (kMaxDim << 1)) return NVFP4_ERR_UNSUPPORTED;
+  if (rows == 0) return NVFP4_OK;
+  // rows without columns have scales (a zero row's)
+  if (s == nullptr || (cols > 0 && (x == nullptr || q == nullptr || ld_x < cols)))
+    return NVFP4_ERR_INVALID_ARG;
+  if (cols > 0 && (!aligned(x, 16) || (ld_x * dtype_size((int)x_dtype)) % 16 != 0 || !aligned(q, 16)))
+    return NVFP4_ERR_UNSUPPORTED;
+  if (!aligned(s, 4)) return NVFP4_ERR_UNSUPPORTED;
   return from_fp8(nvfp4::launch_int8_quantize(x, (int)x_dtype, rows, cols, ld_x, q, s, (hipStream_t)stream));
 }
 

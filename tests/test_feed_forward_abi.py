@@ -89,7 +89,8 @@ QUANT = dict(x=P, x_dtype=BF, rows=4, cols=32, ld_x=32, q=P, s=P)
     (dict(cols=24, ld_x=24), INV), (dict(rows=-1), INV), (dict(x_dtype=2), INV), (dict(ld_x=16), INV),
     (dict(x=None), INV), (dict(q=None), INV), (dict(s=None), INV), (dict(q=None, s=None), INV), (dict(x=P8), UNS),
     (dict(ld_x=36), UNS), (dict(q=P8), UNS), (dict(s=ODD), UNS), (dict(rows=1 << 31), UNS),
-    (dict(rows=1 << 30, cols=65536, ld_x=65536), UNS), (dict(rows=0), OK), (dict(cols=0, ld_x=0), OK),
+    (dict(rows=1 << 30, cols=65536, ld_x=65536), UNS), (dict(rows=0), OK),
+    (dict(rows=0, x=None, q=None, s=None), OK), (dict(cols=0, ld_x=0, s=None), INV),
 ])
 def test_int8_quantize_checks(kw, status):
     assert _call("nvfp4_int8_quantize", QUANT, kw) == status

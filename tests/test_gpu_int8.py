@@ -147,6 +147,9 @@ def test_gemm_empty_and_refusals():
     note("int8 gemm empty")
     assert nv.nvfp4_int8_gemm(e, gpu(b)).shape == (0, 6) and nv.nvfp4_int8_gemm(gpu(a), e).shape == (4, 0)
     assert (nv.nvfp4_int8_gemm(z, z, "f32") == 0).all()
+    q = nv.nvfp4_int8_quantize(torch.zeros(4, 0, device=DEV))
+    same(q, int8_quantize_ref(np.zeros((4, 0), np.float32)))
+    assert (nv.nvfp4_int8_gemm(q, q, "f32") == 0).all()
     with pytest.raises(ValueError):
         nv.nvfp4_int8_gemm(gpu(a), gpu(operand(rng, 6, 80)))
     with pytest.raises(ValueError):
