@@ -379,6 +379,9 @@ hipError_t stream(const Dense& d) {
   return hipGetLastError();
 }
 
+// The FP8 products' rules at N = 2F (fp8_stream.hip and fp8_gemm.hip have both
+// sides of their borders), since loads and loops are theirs; not timed here.  16-row
+// tiles take the 16-bit instructions and their fp32 sums, as there.
 template <bool BROWS, bool WIDE>
 hipError_t dense_any(const Dense& d) {
   const int64_t M = d.M, F = d.F;
@@ -428,7 +431,8 @@ hipError_t grouped_stream(const Grouped& g) {
 }
 
 // The counts are on the device.  Expected tile rows: one for every expert that
-// can have rows, or the rows' worth and half a tile more for each.
+// can have rows, or the rows' worth and half a tile more for each.  The borders are
+// those of the experts' FP8 products at N = 2F, not timed here.
 template <bool GATHER, bool BROWS, bool WIDE>
 hipError_t grouped_any(const Grouped& g) {
   const int64_t live = g.G < g.total_m ? g.G : g.total_m;

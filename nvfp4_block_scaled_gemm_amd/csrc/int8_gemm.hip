@@ -153,6 +153,8 @@ hipError_t stream_cfg(int64_t M, int64_t N, int64_t K, Int8Operand a, Int8Operan
 
 }  // namespace
 
+// The FP8 products' borders and times (fp8_stream.hip, fp8_gemm.hip), whose loads
+// and tiles these are; not timed here.  Every variant gives the same bits.
 hipError_t launch_int8_gemm(int64_t M, int64_t N, int64_t K, Int8Operand a, Int8Operand b, Fp8Out y,
                             hipStream_t stream) {
   if (M <= 16 || tiles_of(M, N, 32, 32) <= 256) {
