@@ -508,8 +508,8 @@ size_t nvfp4_grad_workspace_bytes(int64_t count);
  * one IEEE binary64).  `grads` is a HOST array, read before the call returns;
  * `out` is not read.  Squares and sums are binary64, so nothing finite
  * overflows; their order depends on the list's sizes, types and addresses
- * alone.  A caller whose gradients are spread over processes adds their sums
- * before it clips.  workspace >= nvfp4_grad_workspace_bytes(count) bytes, 8-byte
+ * alone; a tensor listed twice counts twice.  A caller whose gradients are
+ * spread over processes adds their sums before it clips.  workspace >= nvfp4_grad_workspace_bytes(count) bytes, 8-byte
  * aligned, not shared by calls that may overlap.  count == 0 writes 0.
  * Errors: NVFP4_ERR_INVALID_ARG for count < 0, n < 0, a bad dtype, a null
  * pointer (g only where n > 0) or a workspace too small;
