@@ -1114,8 +1114,8 @@ def _gated_inputs(dh, gate_up):
     _need(dh.dim() == 2 and dh.dtype in _DT_IN and dh.is_cuda, "dh: 2-D fp32 or bf16 on a GPU")
     rows, F = dh.shape
     _need(F % 8 == 0, "dh: columns must be a multiple of 8")
-    _need(gate_up.dtype in _DT_IN and tuple(gate_up.shape) == (rows, 2 * F),
-          f"gate_up: expected fp32 or bf16 ({rows}, {2 * F})")
+    if gate_up.dtype not in _DT_IN or gate_up.shape != (rows, 2 * F):
+        raise ValueError(f"gate_up: expected fp32 or bf16 ({rows}, {2 * F})")
     dev = dh.get_device()
     _on_dev(gate_up, dev, "gate_up")
     return rows, F, _stride(dh, F, "dh"), _stride(gate_up, 2 * F, "gate_up"), dev
@@ -1128,20 +1128,27 @@ def nvfp4_fp8_gated_backward(dh: torch.Tensor, gate_up: torch.Tensor, act: str =
     blocks: layout "rows" (q [M, 2F], for dx = [dg, du] . W with W's "cols"
     layout), "cols" (q [2F, M rounded up to 16], for dW = [dg, du]^T . x) or
     "both" as a pair.  ``out`` reuses buffers."""
-    rows, F, ld_dh, ld_gu, dev = _gated_inputs(dh, gate_up)
-    code = _act(act)
-    with contextlib.nullcontext() if _here(stream, dev) else _there(stream, dev):
-        out_r, out_c = _fp8_outs(layout, out)
-        r = c = None
-        if layout != "cols":
-            r = _fp8_buffer(out_r, (rows, 2 * F), (-(-2 * F // 128), rows), 1, dh, dev)
-        if layout != "rows":
-            rows_t = -(-rows // 16) * 16
-            c = _fp8_buffer(out_c, (2 * F, rows_t), (-(-rows_t // 128), 2 * F), 1, dh, dev)
-        st = nvfp4_fp8_gated_backward_raw(_ptr(dh), _DT_IN[dh.dtype], ld_dh, _ptr(gate_up),
-                                          _DT_IN[gate_up.dtype], ld_gu, code, rows, F, *_fp8_ptrs(r, c),
-                                          _stream(None, dev))
-    _check("nvfp4_fp8_gated_backward", st)
+    sizes, code = _gated_inputs(dh, gate_up), _act(act)
+    if _here(stream, sizes[-1]):
+        return _fp8_gated_backward(dh, gate_up, code, layout, out, *sizes)
+    with _there(stream, sizes[-1]):
+        return _fp8_gated_backward(dh, gate_up, code, layout, out, *sizes)
+
+
+def _fp8_gated_backward(dh, gate_up, act: int, layout: str, out, rows: int, F: int, ld_dh: int, ld_gu: int,
+                        dev: int):
+    out_r, out_c = _fp8_outs(layout, out)
+    r = c = None
+    if layout != "cols":
+        r = _fp8_buffer(out_r, (rows, 2 * F), (-(-2 * F // 128), rows), 1, dh, dev)
+    if layout != "rows":
+        rows_t = -(-rows // 16) * 16
+        c = _fp8_buffer(out_c, (2 * F, rows_t), (-(-rows_t // 128), 2 * F), 1, dh, dev)
+    st = nvfp4_fp8_gated_backward_raw(dh.data_ptr(), _DT_IN[dh.dtype], ld_dh, gate_up.data_ptr(),
+                                      _DT_IN[gate_up.dtype], ld_gu, act, rows, F, *_fp8_ptrs(r, c),
+                                      _stream(None, dev))
+    if st != NVFP4_OK:
+        _check("nvfp4_fp8_gated_backward", st)
     return _fp8_result(r, c)
 
 
