@@ -403,7 +403,7 @@ typedef enum {
  * block of 128 rows that ends inside the gate's last 32 costs some time).
  * Both products are summed as in nvfp4_fp8_gemm with an output of h's type
  * and stay in fp32 up to h, which is rounded once.  gate_up (or NULL): bf16
- * [M, 2F], the two products for the backward.  h (F32 or BF16) has row stride
+ * [M, 2F], the two products for the backward, which is that of the rounded ones.  h (F32 or BF16) has row stride
  * ld_h >= F, gate_up ld_gate_up >= 2F elements.  K == 0 writes zeros.
  * Errors as nvfp4_fp8_gemm (2F in the place of N), and
  * NVFP4_ERR_INVALID_ARG for a bad act, NVFP4_ERR_UNSUPPORTED for F > 2^27.
