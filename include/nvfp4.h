@@ -529,7 +529,7 @@ int nvfp4_grad_norm_sq(int64_t count, const nvfp4_grad* grads, double* norm_sq, 
  * that a step can be dropped by looking at norm.  max_norm >= 0 (infinity: never
  * clips).
  * Errors: as above, and NVFP4_ERR_INVALID_ARG for max_norm < 0 or NaN, types
- * that differ in place, or a written tensor that overlaps another one of the
+ * that differ in place (of n > 0), or a written tensor that overlaps another of the
  * list; workspace may be NULL where norm_sq is given.
  */
 int nvfp4_clip_grads(int64_t count, const nvfp4_grad* grads, double max_norm,

@@ -226,10 +226,11 @@ int grad_outs_check(int64_t count, const nvfp4_grad* grads) {
   int64_t n = 0;
   for (int64_t i = 0; i < count; ++i) {
     const nvfp4_grad& g = grads[i];
+    if (!dtype_ok(g.out_dtype)) return NVFP4_ERR_INVALID_ARG;
+    if (g.n == 0) continue;  // its pointers say nothing, not that it is in place either
     const bool in_place = g.out == nullptr || g.out == g.g;
-    if (!dtype_ok(g.out_dtype) || (in_place && g.out_dtype != g.g_dtype)) return NVFP4_ERR_INVALID_ARG;
+    if (in_place && g.out_dtype != g.g_dtype) return NVFP4_ERR_INVALID_ARG;
     if (!aligned(g.out, dtype_size(g.out_dtype))) return NVFP4_ERR_UNSUPPORTED;
-    if (g.n == 0) continue;
     const uintptr_t a = (uintptr_t)g.g, b = (uintptr_t)g.out;
     r[n++] = {a, a + (uintptr_t)(g.n * dtype_size(g.g_dtype)), in_place};
     if (!in_place) r[n++] = {b, b + (uintptr_t)(g.n * dtype_size(g.out_dtype)), true};

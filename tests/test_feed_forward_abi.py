@@ -156,6 +156,18 @@ def test_clip_checks(grads, kw, status):
     assert _call("nvfp4_clip_grads", args, kw) == status
 
 
+@pytest.mark.parametrize("empty", [(0, 0, 0, F32, BF), (0, 0, 0, BF, F32), (A, 0, 0, F32, BF), (A, A, 0, BF, F32)])
+def test_clip_checks_of_empty_tensors(empty):
+    """A tensor without elements has no place and so is not in place: the call passes
+    the list's checks and is refused for what is looked at after them."""
+    arr = _grads((A, B, 16, F32, BF), empty)
+    args = dict(count=2, grads=ctypes.addressof(arr), max_norm=1.0, norm_sq=None, norm=ODD, workspace=P,
+                workspace_bytes=1 << 20)
+    assert _call("nvfp4_clip_grads", args, {}) == UNS
+    arr[1].out_dtype = 2
+    assert _call("nvfp4_clip_grads", args, {}) == INV
+
+
 def test_clip_checks_long_lists():
     rows = [(A + 64 * i, 0, 16, F32, F32) for i in range(300)]
     arr = _grads(*rows, (A + 64 * 150 + 4, 0, 1, F32, F32))

@@ -197,3 +197,15 @@ def test_clip_of_a_tensor_past_31_bits():
     assert abs(float(top) - norm) <= 2.0 ** -23 * norm
     assert float(out[-1]) == 1.5 and float(out[1 << 31]) == 1.0 and bool((out[: 1 << 31] == 0.5).all())
     assert bool((out[(1 << 31) + 1:-1] == 0.5).all())
+
+
+@pytest.mark.parametrize("dt,odt", [(torch.float32, torch.bfloat16), (torch.bfloat16, torch.float32)])
+def test_empty_tensors_into_another_type(dt, odt):
+    grads = [torch.randn(n, generator=torch.Generator().manual_seed(n)).to(dt) for n in (5, 0, 300, 0)]
+    on = [g.to(DEV) for g in grads]
+    norm, _, _ = clip_ref([np_(g) for g in grads], 1.0)
+    note(f"clip with empty tensors {dt} -> {odt}")
+    out = [torch.empty(g.shape, dtype=odt, device=DEV) for g in on]
+    n = nv.nvfp4_clip_grads(on, 0.4 * norm, out=out)
+    assert abs(float(n) - norm) <= 2.0 ** -23 * norm
+    check(out, grads, 0.4)
