@@ -41,8 +41,9 @@ __device__ __forceinline__ void gradients8(const GatedIn& in, int64_t r, int64_t
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const Sigma a = sigma_of<decltype(act)::value>(g[j]);
-      dg[j] = d[j] * u[j] * (a.sigma * a.slope);
-      du[j] = d[j] * (g[j] * a.sigma);
+      const float v = g[j] * a.sigma;
+      dg[j] = d[j] * u[j] * __builtin_fmaf(v, a.turn, a.sigma);
+      du[j] = d[j] * v;
     }
   };
   if (in.act == kGelu) all(std::integral_constant<int, kGelu>{});

@@ -424,3 +424,66 @@ def test_gated_far_rows():
     at = torch.from_numpy(rows).to(DEV)
     few = nv.nvfp4_fp8_gated_backward(h[at], kept[at], layout="rows")
     assert torch.equal(r[0][at].view(torch.uint8), few[0].view(torch.uint8)) and torch.equal(r[1][:, at], few[1])
+
+
+# ---- the activations' tails ----------------------------------------------------
+
+TAILS = {"silu": [-70, -86.5, -87, -87.5, -88, -90, -95, -100, -102.5, -104, -106, -150, 87, 88, 104, 150, 0.0, 1e-30],
+         "gelu": [-9, -9.8, -9.9, -9.95, -10, -10.1, -10.2, -10.3, -10.5, -10.6, -10.8, -15, 9.9, 10, 10.7, 15, 0.0, 1e-30]}
+
+
+def tail_error(g, act):
+    """Largest error of sigma(z(g)) in fp32: relative, 8 roundings and gelu's z off by
+    4 more (each moves exp by |z| 2^-24); below the normal numbers two roundings to
+    multiples of 2^-149."""
+    z = np.abs(g) if act == "silu" else 2 * np.sqrt(2 / np.pi) * (np.abs(g) + 0.044715 * np.abs(g) ** 3)
+    sigma = np.where(g >= 0, 1.0, np.exp(-z))
+    return (8 + (4 * z if act == "gelu" else 0)) * 2.0 ** -24 * sigma + 2 * 2.0 ** -150
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("M", [2, 100])
+def test_gated_tails(act, M):
+    """Gates whose sigma is small or below the normal numbers, times an up projection
+    that brings their products back: act(g) is not cut to zero."""
+    K, F = 128, 32
+    gate = np.resize(np.array(TAILS[act], np.float32), F)
+    q, w = np.zeros((M, K), np.uint8), np.zeros((2 * F, K), np.uint8)
+    q[:, 0] = w[:, 0] = 0x38                                 # 1
+    up = 2.0 ** 100
+    s = np.concatenate([gate, np.full(F, up, np.float32)])[None]
+    g = gate.astype(np.float64)
+    v = act_ref(g, act)[0]
+    # g sigma rounds (below the normal numbers by up to 2^-150), and so does its product
+    tol = up * (np.abs(g) * tail_error(g, act) + 2.0 ** -150) + 2 * 2.0 ** -24 * np.abs(v * up)
+    note(f"fp8 gated tails {act} M {M}")
+    for out in ("f32", "bf16"):
+        h = np_(nv.nvfp4_fp8_gated_gemm(gpu((q, np.ones((1, M), np.float32))), gpu((w, s)), act, out)).astype(np.float64)
+        t = tol if out == "f32" else tol + 2.0 ** -8 * (np.abs(v * up) + tol)
+        bad = np.argwhere(~(np.abs(h - v * up) <= t))
+        assert bad.size == 0, [(gate[j], h[i, j], (v * up)[j], t[j]) for i, j in bad[:4]]
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_backward_tails(act):
+    """The same of the gradients, one to a block (the transposed layout of one row), so
+    that a scale shows its value."""
+    gate = np.resize(np.array(TAILS[act], np.float32), 64)
+    g, up = gate.astype(np.float64), 2.0 ** 60
+    v, d = act_ref(g, act)
+    sig = np.where(g == 0, 0.5, v / np.where(g == 0, 1.0, g))
+    # |g z'| of act' = sigma + g sigma z' (1 - sigma)
+    far = np.abs(g) if act == "silu" else 2 * np.sqrt(2 / np.pi) * (np.abs(g) + 3 * 0.044715 * np.abs(g) ** 3)
+    dh, u = np.full(64, 2.0 ** 60, np.float32), np.full(64, up, np.float32)
+    e = tail_error(g, act)
+    dg, du = 2.0 ** 120 * d, 2.0 ** 60 * v
+    parts = np.abs(sig) + np.abs(d - sig)
+    # sigma's error in both parts (their 1 - sigma has it too where it is small), 8 roundings
+    # more; a part below the normal numbers rounds by up to 2^-150
+    err_dg = 2.0 ** 120 * ((1 + far) * 2 * e + 8 * 2.0 ** -24 * parts + (2 + far) * 2.0 ** -150)
+    err_du = 2.0 ** 60 * (np.abs(g) * e + 2.0 ** -150) + 2 * 2.0 ** -24 * np.abs(du)
+    note(f"fp8 gated backward tails {act}")
+    c = nv.nvfp4_fp8_gated_backward(torch.from_numpy(dh)[None].to(DEV),
+                                    torch.from_numpy(np.concatenate([gate, u]))[None].to(DEV), act, layout="cols")
+    ref, err = np.concatenate([dg, du])[None], np.concatenate([err_dg, err_du])[None]
+    check_operand(c, turned(ref, 16), turned(err, 16), "cols")
