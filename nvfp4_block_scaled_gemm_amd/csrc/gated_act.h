@@ -47,7 +47,11 @@ __device__ __forceinline__ Sigma sigma_of(float g) {
   }
   // (a NaN is lost in the minima, not in the product with g)
   const float t = exp_near(-__builtin_fminf(__builtin_fabsf(z), kEdge));
-  const float large = __builtin_amdgcn_rcpf(1.0f + t), small = t * large;
+  // 1 / (1 + t), with what the sum rounds off and what the hardware's reciprocal leaves put
+  // back: one rounding instead of three
+  const float sum = 1.0f + t, near = __builtin_amdgcn_rcpf(sum);
+  const float left = __builtin_fmaf(-(t - (sum - 1.0f)), near, __builtin_fmaf(-sum, near, 1.0f));
+  const float large = __builtin_fmaf(near, left, near), small = t * large;
   return {z >= 0.0f ? large : small, slope * (z >= 0.0f ? small : large)};
 }
 

@@ -487,3 +487,21 @@ def test_backward_tails(act):
                                     torch.from_numpy(np.concatenate([gate, u]))[None].to(DEV), act, layout="cols")
     ref, err = np.concatenate([dg, du])[None], np.concatenate([err_dg, err_du])[None]
     check_operand(c, turned(ref, 16), turned(err, 16), "cols")
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_backward_rounds_as_fp32(act):
+    """The slope's rounding errors over normal gates, in rms: a rounding to fp32 is off by
+    2^-24 / sqrt(3) / m of the value, m its significand, 2^-24 * 0.577 * 0.7355 = 2.53e-8 in rms
+    for m spread over its logarithm.  act' = sigma + act turn rounds once itself and takes
+    over sigma's rounding; act, turn and the exponential (three roundings, the hardware's
+    exp2 off by one unit) reach it with weights around 1/4: sqrt(2 + 5/16) = 1.52
+    roundings.  The scale that shows it adds one: sqrt(2 + 5/16 + 1) = 1.82.  Not more
+    than 2.1 of them; a rounding more in sigma (1 + t, or its reciprocal) gives 2.1 to 2.3."""
+    g = torch.randn(1, 8192, generator=torch.Generator().manual_seed(7)) * 1.5
+    gu, dh = torch.cat([g, torch.ones_like(g)], 1), torch.ones_like(g)
+    note(f"fp8 gated backward rounding {act}")
+    c = nv.nvfp4_fp8_gated_backward(dh.to(DEV), gu.to(DEV), act, layout="cols")
+    got = np_(c[1]).astype(np.float64)[0, :8192] * 448
+    want = np.abs(act_ref(g.numpy()[0], act)[1])
+    assert np.linalg.norm(got - want) <= 2.1 * 2.53e-8 * np.linalg.norm(want)
