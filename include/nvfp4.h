@@ -419,7 +419,7 @@ int nvfp4_fp8_gated_gemm(int64_t M, int64_t F, int64_t K, const uint8_t* a_q, co
  * The same per expert: group e's rows of a times w_q + e*2F*K,
  * w_s [G, ceil(K/128), ceil(2F/128)] (block_rows 128), with m_offsets, row_index
  * and a_rows as in nvfp4_fp8_grouped_gemm.  Rows of h and gate_up of no group
- * are left as they were.
+ * are left as they were.  NVFP4_ERR_UNSUPPORTED for G > 2^30 too.
  */
 int nvfp4_fp8_grouped_gated_gemm(int32_t G, const int32_t* m_offsets, const int32_t* row_index,
                                  int64_t total_m, int64_t a_rows, int64_t F, int64_t K,
@@ -450,7 +450,8 @@ int nvfp4_fp8_gated_backward(const void* dh, nvfp4_dtype dh_dtype, int64_t ld_dh
 /*
  * The same for rows sorted by group: layouts, padding columns and rows of no
  * group as in nvfp4_fp8_grouped_quantize (cols = 2F), for
- * nvfp4_fp8_grouped_gemm and nvfp4_fp8_grouped_wgrad.
+ * nvfp4_fp8_grouped_gemm and nvfp4_fp8_grouped_wgrad.  NVFP4_ERR_UNSUPPORTED
+ * for G > 2^30 too.
  */
 int nvfp4_fp8_grouped_gated_backward(int32_t G, const int32_t* m_offsets, const void* dh,
                                      nvfp4_dtype dh_dtype, int64_t ld_dh, const void* gate_up,

@@ -564,7 +564,7 @@ int nvfp4_fp8_grouped_gated_gemm(int32_t G, const int32_t* m_offsets, const int3
   if (G < 0 || total_m < 0 || F < 0 || K < 0 || K % 16 != 0) return NVFP4_ERR_INVALID_ARG;
   if ((G == 0 && total_m != 0) || a_rows < 0 || !act_ok((int)act)) return NVFP4_ERR_INVALID_ARG;
   if (row_index == nullptr && a_rows != 0 && a_rows != total_m) return NVFP4_ERR_INVALID_ARG;
-  if (total_m > kMaxDim || a_rows > kMaxDim || F > kMaxGated || K > kMaxFp8K)
+  if (G > kMaxDim || total_m > kMaxDim || a_rows > kMaxDim || F > kMaxGated || K > kMaxFp8K)
     return NVFP4_ERR_UNSUPPORTED;
   if (total_m == 0 || F == 0) return NVFP4_OK;
   if (m_offsets == nullptr) return NVFP4_ERR_INVALID_ARG;
@@ -593,6 +593,7 @@ int nvfp4_fp8_grouped_gated_backward(int32_t G, const int32_t* m_offsets, const 
                                      int64_t total_m, int64_t F, uint8_t* q, float* s, uint8_t* qt,
                                      float* st, void* stream) {
   if (G < 0 || (G == 0 && total_m != 0)) return NVFP4_ERR_INVALID_ARG;
+  if (G > kMaxDim) return NVFP4_ERR_UNSUPPORTED;
   const nvfp4::GatedGradient g{dh, gate_up, ld_dh, ld_gate_up, F, (int)dh_dtype, (int)gate_up_dtype, (int)act};
   const int v = gated_backward_check(g, total_m, q, s, qt, st);
   if (v != NVFP4_OK) return v == 1 ? NVFP4_OK : v;

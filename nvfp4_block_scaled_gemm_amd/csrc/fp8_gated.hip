@@ -135,7 +135,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gated_grouped_kernel(
       A = {a.q, a.s, a_rows, (uint32_t)(a_rows * K), (uint32_t)a_rows * 4, row_index + m0, rm, (int32_t)a_rows};
     else
       A = rows_of(a, total_m, m0, rm, K);
-    const TileOperand B = weight_of(b.q + e * 2 * F * K, b.s + e * kb * nb, nb, 7, n0, rn, F, K);
+    const TileOperand B = weight_of(b.q + (int64_t)e * 2 * F * K, b.s + e * kb * nb, nb, 7, n0, rn, F, K);
     T::template run<GATHER>(A, B, (uint32_t)K, (uint32_t)K, out_of(y, m0, n0, rm, rn), smem);
     workgroup_barrier();  // every wave is past its last fragment reads
   }

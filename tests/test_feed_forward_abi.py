@@ -82,6 +82,16 @@ def test_grouped_backward_needs_groups():
         assert _call("nvfp4_fp8_grouped_gated_backward", grouped, kw) == status
 
 
+def test_gated_calls_of_too_many_groups():
+    """Experts are counted in 32 bits, an expert's rows of its weight twice over."""
+    many = (1 << 30) + 1
+    assert _call("nvfp4_fp8_grouped_gated_gemm", GGATED, dict(G=many)) == UNS
+    assert _call("nvfp4_fp8_grouped_gated_gemm", GGATED, dict(G=many, row_index=P)) == UNS
+    assert _call("nvfp4_fp8_grouped_gated_backward", dict(G=2, m_offsets=P, **BACK), dict(G=many)) == UNS
+    for kw in (dict(G=many, total_m=0, a_rows=0), dict(G=many, F=0)):
+        assert _call("nvfp4_fp8_grouped_gated_gemm", GGATED, kw) == UNS
+
+
 QUANT = dict(x=P, x_dtype=BF, rows=4, cols=32, ld_x=32, q=P, s=P)
 
 
