@@ -321,7 +321,8 @@ int64_t nvfp4_fp8_grouped_columns(int64_t total_m, int32_t G);
  *                groups; columns of no token are zero.
  * row_index (or NULL): grouped row r is row row_index[r] of x [x_rows, cols];
  * an index outside [0, x_rows) is a row of zeros.  Without it x has total_m
- * rows and x_rows is not read.  Errors as above.
+ * rows and x_rows is not read.  Errors as above, and NVFP4_ERR_UNSUPPORTED for
+ * G > 2^31 - 65.
  */
 int nvfp4_fp8_grouped_quantize(const void* x, nvfp4_dtype x_dtype, int32_t G,
                                const int32_t* m_offsets, const int32_t* row_index,
@@ -367,7 +368,7 @@ int nvfp4_fp8_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a_q, const fl
  * they were.  Without row_index a has total_m rows and a_rows must be 0 or
  * total_m.  The input gradient is the same call with dy and the transposed
  * weights.  Sums and errors as nvfp4_fp8_gemm, and NVFP4_ERR_UNSUPPORTED for
- * a_rows * K >= 2^31 with row_index.
+ * G > 2^31 - 65, or a_rows * K >= 2^31 with row_index.
  */
 int nvfp4_fp8_grouped_gemm(int32_t G, const int32_t* m_offsets, const int32_t* row_index,
                            int64_t total_m, int64_t a_rows, int64_t N, int64_t K,

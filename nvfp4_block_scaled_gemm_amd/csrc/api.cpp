@@ -15,6 +15,7 @@
 namespace {
 
 constexpr int64_t kMaxDim = (int64_t)1 << 30;  // keeps 32-bit tile indexing safe
+constexpr int32_t kMaxGroups = INT32_MAX - 64;  // experts' walks count them in 64s
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
@@ -475,7 +476,7 @@ int nvfp4_fp8_grouped_quantize(const void* x, nvfp4_dtype x_dtype, int32_t G,
                                uint8_t* q, float* s, uint8_t* qt, float* st, void* stream) {
   if (G < 0 || (G == 0 && total_m != 0)) return NVFP4_ERR_INVALID_ARG;
   if (row_index != nullptr && x_rows < 0) return NVFP4_ERR_INVALID_ARG;
-  if (row_index != nullptr && x_rows > kMaxDim) return NVFP4_ERR_UNSUPPORTED;
+  if (G > kMaxGroups || (row_index != nullptr && x_rows > kMaxDim)) return NVFP4_ERR_UNSUPPORTED;
   const int v = fp8_quantize_check(x, (int)x_dtype, total_m, cols, ld_x, q, s, qt, st);
   if (v != NVFP4_OK) return v == 1 ? NVFP4_OK : v;
   if (m_offsets == nullptr) return NVFP4_ERR_INVALID_ARG;
@@ -507,7 +508,7 @@ int nvfp4_fp8_grouped_gemm(int32_t G, const int32_t* m_offsets, const int32_t* r
   if (G < 0 || total_m < 0 || N < 0 || K < 0 || K % 16 != 0) return NVFP4_ERR_INVALID_ARG;
   if ((G == 0 && total_m != 0) || a_rows < 0) return NVFP4_ERR_INVALID_ARG;
   if (row_index == nullptr && a_rows != 0 && a_rows != total_m) return NVFP4_ERR_INVALID_ARG;
-  if (total_m > kMaxDim || a_rows > kMaxDim || N > kMaxDim || K > kMaxFp8K)
+  if (G > kMaxGroups || total_m > kMaxDim || a_rows > kMaxDim || N > kMaxDim || K > kMaxFp8K)
     return NVFP4_ERR_UNSUPPORTED;
   if (total_m == 0 || N == 0) return NVFP4_OK;
   if (m_offsets == nullptr) return NVFP4_ERR_INVALID_ARG;

@@ -100,6 +100,16 @@ def test_grouped_checks(kw, status):
     assert _call("nvfp4_fp8_grouped_gemm", GROUPED, kw) == status
 
 
+def test_the_walk_over_groups_ends():
+    """The kernels take 64 groups at a time and count them in 32 bits: past 2^31 - 65 the
+    count would turn negative before it reaches the end."""
+    for G in ((1 << 31) - 64, (1 << 31) - 1):
+        assert _call("nvfp4_fp8_grouped_gemm", GROUPED, dict(G=G)) == UNS
+        assert _call("nvfp4_fp8_grouped_gemm", GROUPED, dict(G=G, N=1 << 20, ld_y=1 << 20)) == UNS
+        assert _call("nvfp4_fp8_grouped_quantize", GQUANT, dict(G=G)) == UNS
+    assert _call("nvfp4_fp8_grouped_gemm", GROUPED, dict(G=(1 << 31) - 65, total_m=0)) == OK
+
+
 WGRAD = dict(G=4, m_offsets=P, total_m=8, N=8, K=8, a_q=P, a_s=P, b_q=P, b_s=P, dw=P, dw_dtype=nv.NVFP4_F32,
              flags=0)
 
