@@ -513,10 +513,12 @@ size_t nvfp4_grad_workspace_bytes(int64_t count);
  * `out` is not read.  Squares and sums are binary64, so nothing finite
  * overflows; their order depends on the list's sizes, types and addresses
  * alone; a tensor listed twice counts twice.  A caller whose gradients are
- * spread over processes adds their sums before it clips.  workspace >= nvfp4_grad_workspace_bytes(count) bytes, 8-byte
- * aligned, not shared by calls that may overlap.  count == 0 writes 0.
+ * spread over processes adds their sums before it clips.  workspace:
+ * nvfp4_grad_workspace_bytes(count) bytes or more, 8-byte aligned, not shared by
+ * calls that may overlap.  count == 0 writes 0.
  * Errors: NVFP4_ERR_INVALID_ARG for count < 0, n < 0, a bad dtype, a null
- * pointer (g only where n > 0) or a workspace too small;
+ * pointer (g only where n > 0), or a workspace that is too small or overlaps a
+ * gradient;
  * NVFP4_ERR_UNSUPPORTED for pointers not aligned to their elements, or more
  * than 2^42 elements or 2^20 tensors.
  */
@@ -533,8 +535,10 @@ int nvfp4_grad_norm_sq(int64_t count, const nvfp4_grad* grads, double* norm_sq, 
  * that a step can be dropped by looking at norm.  max_norm >= 0 (infinity: never
  * clips).
  * Errors: as above, and NVFP4_ERR_INVALID_ARG for max_norm < 0 or NaN, types
- * that differ in place (of n > 0), or a written tensor that overlaps another of the
- * list; workspace may be NULL where norm_sq is given.
+ * that differ in place (of n > 0), a written tensor that overlaps another of the
+ * list; for norm or the workspace overlapping a tensor of the list, norm_sq one
+ * that is written, or norm overlapping the workspace or norm_sq.  workspace may be
+ * NULL where norm_sq is given, and is not used then.
  */
 int nvfp4_clip_grads(int64_t count, const nvfp4_grad* grads, double max_norm,
                      const double* norm_sq, float* norm, void* workspace, size_t workspace_bytes,

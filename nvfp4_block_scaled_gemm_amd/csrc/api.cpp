@@ -212,13 +212,37 @@ int grads_check(int64_t count, const nvfp4_grad* grads) {
   return NVFP4_OK;
 }
 
-// Outputs: their types and alignment, and that no written tensor overlaps
-// another one (each would be scaled by whoever comes first).
+bool in_place(const nvfp4_grad& g) { return g.out == nullptr || g.out == g.g; }
+
+// Outputs: their types and alignment.  A tensor without elements is nowhere, so it is not
+// in place either.
 int grad_outs_check(int64_t count, const nvfp4_grad* grads) {
-  struct Range {
-    uintptr_t begin, end;
-    bool written;
-  };
+  for (int64_t i = 0; i < count; ++i) {
+    const nvfp4_grad& g = grads[i];
+    if (!dtype_ok(g.out_dtype)) return NVFP4_ERR_INVALID_ARG;
+    if (g.n == 0) continue;
+    if (in_place(g) && g.out_dtype != g.g_dtype) return NVFP4_ERR_INVALID_ARG;
+    if (!aligned(g.out, dtype_size(g.out_dtype))) return NVFP4_ERR_UNSUPPORTED;
+  }
+  return NVFP4_OK;
+}
+
+struct Range {
+  uintptr_t begin, end;
+  bool written;
+};
+Range range_of(const void* p, int64_t bytes, bool written) {
+  return {(uintptr_t)p, (uintptr_t)p + (uintptr_t)(p == nullptr ? 0 : bytes), written};
+}
+bool overlap(const Range& x, const Range& y) { return x.begin < y.end && y.begin < x.end; }
+Range read_by(const nvfp4_grad& g, bool scaled) {
+  return range_of(g.g, g.n * dtype_size(g.g_dtype), scaled && in_place(g));
+}
+Range written_by(const nvfp4_grad& g) { return range_of(g.out, g.n * dtype_size(g.out_dtype), true); }
+
+// That no written tensor overlaps another one (each would be scaled by whoever comes
+// first).
+int grad_overlap_check(int64_t count, const nvfp4_grad* grads) {
   Range few[256];
   std::unique_ptr<Range[]> many;
   if (count > 128) many.reset(new (std::nothrow) Range[2 * count]);
@@ -226,15 +250,9 @@ int grad_outs_check(int64_t count, const nvfp4_grad* grads) {
   Range* r = count > 128 ? many.get() : few;
   int64_t n = 0;
   for (int64_t i = 0; i < count; ++i) {
-    const nvfp4_grad& g = grads[i];
-    if (!dtype_ok(g.out_dtype)) return NVFP4_ERR_INVALID_ARG;
-    if (g.n == 0) continue;  // its pointers say nothing, not that it is in place either
-    const bool in_place = g.out == nullptr || g.out == g.g;
-    if (in_place && g.out_dtype != g.g_dtype) return NVFP4_ERR_INVALID_ARG;
-    if (!aligned(g.out, dtype_size(g.out_dtype))) return NVFP4_ERR_UNSUPPORTED;
-    const uintptr_t a = (uintptr_t)g.g, b = (uintptr_t)g.out;
-    r[n++] = {a, a + (uintptr_t)(g.n * dtype_size(g.g_dtype)), in_place};
-    if (!in_place) r[n++] = {b, b + (uintptr_t)(g.n * dtype_size(g.out_dtype)), true};
+    if (grads[i].n == 0) continue;
+    r[n++] = read_by(grads[i], true);
+    if (!in_place(grads[i])) r[n++] = written_by(grads[i]);
   }
   std::sort(r, r + n, [](const Range& x, const Range& y) { return x.begin < y.begin; });
   uintptr_t read_to = 0, written_to = 0;  // ends of what starts before
@@ -242,6 +260,18 @@ int grad_outs_check(int64_t count, const nvfp4_grad* grads) {
     if (r[i].begin < written_to || (r[i].written && r[i].begin < read_to)) return NVFP4_ERR_INVALID_ARG;
     uintptr_t& to = r[i].written ? written_to : read_to;
     to = std::max(to, r[i].end);
+  }
+  return NVFP4_OK;
+}
+
+// That memory of the call itself lies apart from the tensors: what it writes from all of
+// them, what it reads from those that are written (scaled: the call writes tensors).
+int grad_apart_check(int64_t count, const nvfp4_grad* grads, bool scaled, const Range& own) {
+  for (int64_t i = 0; i < count; ++i) {
+    if (grads[i].n == 0) continue;
+    const Range g = read_by(grads[i], scaled);
+    if ((own.written || g.written) && overlap(own, g)) return NVFP4_ERR_INVALID_ARG;
+    if (scaled && !in_place(grads[i]) && overlap(own, written_by(grads[i]))) return NVFP4_ERR_INVALID_ARG;
   }
   return NVFP4_OK;
 }
@@ -646,6 +676,8 @@ int nvfp4_grad_norm_sq(int64_t count, const nvfp4_grad* grads, double* norm_sq, 
   v = grad_workspace_check(count, workspace, workspace_bytes);
   if (v != NVFP4_OK) return v;
   if (!aligned(norm_sq, 8)) return NVFP4_ERR_UNSUPPORTED;
+  v = grad_apart_check(count, grads, false, range_of(workspace, nvfp4::grad_workspace_bytes(count), true));
+  if (v != NVFP4_OK) return v;
   return from_hip(nvfp4::launch_grad_norm_sq(count, grads, norm_sq, (double*)workspace, (hipStream_t)stream));
 }
 
@@ -659,6 +691,14 @@ int nvfp4_clip_grads(int64_t count, const nvfp4_grad* grads, double max_norm,
   if (norm_sq == nullptr) v = grad_workspace_check(count, workspace, workspace_bytes);
   if (v != NVFP4_OK) return v;
   if (!aligned(norm_sq, 8) || !aligned(norm, 4)) return NVFP4_ERR_UNSUPPORTED;
+  v = grad_overlap_check(count, grads);
+  const Range sums = norm_sq != nullptr ? range_of(norm_sq, 8, false)
+                                        : range_of(workspace, nvfp4::grad_workspace_bytes(count), true);
+  const Range result = range_of(norm, 4, true);
+  if (v == NVFP4_OK) v = grad_apart_check(count, grads, true, sums);
+  if (v == NVFP4_OK) v = grad_apart_check(count, grads, true, result);
+  if (v == NVFP4_OK && overlap(result, sums)) v = NVFP4_ERR_INVALID_ARG;
+  if (v != NVFP4_OK) return v;
   return from_hip(nvfp4::launch_clip_grads(count, grads, max_norm, norm_sq, norm, (double*)workspace,
                                            (hipStream_t)stream));
 }

@@ -178,6 +178,38 @@ def test_clip_checks_of_empty_tensors(empty):
     assert _call("nvfp4_clip_grads", args, {}) == INV
 
 
+FAR = ctypes.c_void_p(0x800000)
+
+
+def _at(address):
+    return ctypes.c_void_p(address)
+
+
+@pytest.mark.parametrize("grads,kw", [
+    ([(A, 0, 16, F32, F32)], dict(norm=_at(A + 60))), ([(A, B, 16, F32, F32)], dict(norm=_at(A))),
+    ([(A, B, 16, F32, BF)], dict(norm=_at(B + 28))),
+    ([(A, 0, 16, F32, F32)], dict(workspace=_at(A + 56))), ([(A, B, 16, F32, F32)], dict(workspace=_at(B - (1 << 16)))),
+    ([(A, 0, 16, F32, F32)], dict(norm_sq=_at(A + 8))), ([(A, B, 16, F32, F32)], dict(norm_sq=_at(B))),
+    ([(A, B, 16, F32, F32)], dict(norm=_at(0x900004), norm_sq=_at(0x900000))),
+    ([(A, B, 16, F32, F32)], dict(norm=_at(0x900000), norm_sq=_at(0x900000))),
+    ([(A, B, 16, F32, F32)], dict(norm=_at(0x800010))),
+])
+def test_clip_checks_of_its_own_memory(grads, kw):
+    """Workgroups read the squared norm, the workspace and the gradients while others
+    write: none of what is written may lie in what is read, or in another result."""
+    arr = _grads(*grads)
+    args = dict(count=len(grads), grads=ctypes.addressof(arr), max_norm=1.0, norm_sq=None, norm=_at(0x700000),
+                workspace=FAR, workspace_bytes=1 << 20)
+    assert _call("nvfp4_clip_grads", args, kw) == INV
+
+
+def test_norm_checks_of_its_workspace():
+    for at in (A, A + 56, A - 8):
+        arr = _grads((A, 0, 16, F32, F32))
+        args = dict(count=1, grads=ctypes.addressof(arr), norm_sq=FAR, workspace=_at(at), workspace_bytes=1 << 20)
+        assert _call("nvfp4_grad_norm_sq", args, {}) == INV
+
+
 def test_clip_checks_long_lists():
     rows = [(A + 64 * i, 0, 16, F32, F32) for i in range(300)]
     arr = _grads(*rows, (A + 64 * 150 + 4, 0, 1, F32, F32))
