@@ -25,6 +25,7 @@ struct Sigma {
 // below the normal numbers: there it takes t + 32 (exact, since it is nearer to zero), and
 // the result is scaled back.
 __device__ __forceinline__ float exp_near(float x) {
+#pragma clang fp contract(off)  // t + 32 is that of the rounded t, whose error r holds
   constexpr float kLog2e = 1.44269504088896340736f, kLog2eLow = 1.925963033500e-8f;
   constexpr float kLn2 = 0.69314718055994530942f;
   const float t = x * kLog2e;
