@@ -25,8 +25,8 @@ OUT = os.path.join(ROOT, "_build", "host")
 CLANG = "/opt/rocm/llvm/bin/clang++"
 SOURCES = ("api.cpp", "fp8_gated.hip", "fp8_gated_backward.hip", "fp8_gemm.hip", "fp8_quantize.hip", "fp8_stream.hip",
            "grad_clip.hip", "int8_gemm.hip", "int8_quantize.hip")
-FLAGS = ["-std=c++17", "-O1", "-g1", "-fPIC", "-w", "-fno-strict-aliasing", "-ffp-contract=off", "-msse4.1", "-mf16c",
-         "-Xarch_host", "-fsanitize=address", "-mllvm", "-asan-stack=0"]
+FLAGS = ["-std=c++17", "-O1", "-g1", "-fPIC", "-w", "-fno-strict-aliasing", "-mfma", "-mf16c",
+         "-ffp-contract=fast-honor-pragmas", "-Xarch_host", "-fsanitize=address", "-mllvm", "-asan-stack=0"]
 
 
 def sanitizer():
@@ -36,7 +36,10 @@ def sanitizer():
 
 
 def available() -> bool:
-    return platform.machine() == "x86_64" and os.path.exists(CLANG) and sanitizer() is not None
+    if platform.machine() != "x86_64" or not os.path.exists(CLANG) or sanitizer() is None:
+        return False
+    with open("/proc/cpuinfo") as fh:
+        return {"fma", "f16c"} <= set(fh.read().split())
 
 
 def _launches(text: str) -> str:
