@@ -404,10 +404,14 @@ typedef enum {
  * product of the FP8 operands a = x [M, K] (block_rows 1) and w = [Wg; Wu]
  * [2F, K] (gate rows first; w_block_rows 1 or 128; F of any size, though a
  * block of 128 rows that ends inside the gate's last 32 costs some time).
- * Both products are summed as in nvfp4_fp8_gemm with an output of h's type
- * and stay in fp32 up to h, which is rounded once.  gate_up (or NULL): bf16
- * [M, 2F], the two products for the backward, which is that of the rounded ones.  h (F32 or BF16) has row stride
- * ld_h >= F, gate_up ld_gate_up >= 2F elements.  K == 0 writes zeros.
+ * Both products are summed as in nvfp4_fp8_gemm with an output of h's type: an
+ * F32 h has fp32 sums; with a BF16 h either factor may be off by what that call
+ * states of the 8-bit instructions, before act and the product, and by up to 16 rows
+ * (which keep fp32 sums) a row of h can differ from its value in a larger batch.
+ * They stay in fp32 up to h, which is rounded once.  gate_up (or NULL): bf16
+ * [M, 2F], the two products for the backward, which is that of the rounded ones.
+ * h (F32 or BF16) has row stride ld_h >= F, gate_up ld_gate_up >= 2F elements.
+ * K == 0 writes zeros.
  * Errors as nvfp4_fp8_gemm (2F in the place of N), and
  * NVFP4_ERR_INVALID_ARG for a bad act, NVFP4_ERR_UNSUPPORTED for F > 2^27.
  */

@@ -582,7 +582,8 @@ def _here(stream, dev: int) -> bool:
 
 def _stride(t, cols: int, what: str) -> int:
     """Row stride of a 2-D tensor whose rows must be contiguous (a single
-    row's stride says nothing, so its length stands in)."""
+    row's stride says nothing, so its length stands in; neither do those of a
+    tensor without elements, which passes whatever its order)."""
     _need(t.stride(-1) == 1 or cols <= 1 or t.numel() == 0, f"{what}: rows must have unit column stride")
     return t.stride(-2) if t.shape[-2] > 1 else cols
 

@@ -110,9 +110,11 @@ struct ExpertTiles {
 };
 
 // Experts' rows: workgroups walk the tiles, tile rows fastest so that
-// neighbours share a weight tile.  (In the 256 x 256 shape the walk costs 6 to 12
-// spilled registers, stored before and read after a tile's loop over K, never in
-// it; the other shapes and the dense kernels have none.)
+// neighbours share a weight tile.  (The walk and three outputs' addresses spill 56 to
+// 70 scalar registers into lanes of vector registers in every shape, where the plain
+// experts' product spills 21 to 35, and 6 to 12 vector registers in the 256 x 256 shape:
+// stored before and read after a tile's loop over K, never in it.  The dense kernels
+// spill nothing.)
 template <int BM, int BN, int WM, int WN, int STAGES, bool GATHER, bool BROWS, bool WIDE>
 __global__ __launch_bounds__(64 * WM * WN, 2) void gated_grouped_kernel(
     int G, const int32_t* __restrict__ offsets, const int32_t* __restrict__ row_index, int64_t total_m,
@@ -381,9 +383,13 @@ hipError_t stream(const Dense& d) {
   return hipGetLastError();
 }
 
-// The FP8 products' rules at N = 2F (fp8_stream.hip and fp8_gemm.hip have both
-// sides of their borders), since loads and loops are theirs; not timed here.  16-row
-// tiles take the 16-bit instructions and their fp32 sums, as there.
+// The FP8 products' times at N = 2F (fp8_stream.hip, fp8_gemm.hip), since loads and
+// loops are theirs; no border was measured here.  Their shapes for 17 to some 600
+// rows are missing: 64 x 64 and 128 x 64, whose waves take 32 weight rows and split K
+// in two (a wave's 64 rows hold both projections here).  By those times M = 32, F = K =
+// 8192 takes 128 tiles of 64 x 128 and 0.60 us a block of K, where the plain product of
+// 2F columns takes 0.35: 38 us against 22 and an activation.  16-row tiles take the
+// 16-bit instructions and their fp32 sums, as there.
 template <bool BROWS, bool WIDE>
 hipError_t dense_any(const Dense& d) {
   const int64_t M = d.M, F = d.F;

@@ -12,8 +12,10 @@
 // three inputs into the two tiles of dg and du, so the inputs are read once;
 // for other F a block of 128 columns straddles the halves and each workgroup
 // computes one output tile (its inputs are read twice, the second time mostly
-// from a cache).  The rows layout alone needs no shared memory: 16 lanes take
-// one 1 x 128 block.
+// from a cache).  Both gradients and what they come from take 150 registers: one
+// workgroup of eight waves on a CU, where the quantiser's 76 leave room for three.
+// The rows layout alone needs no shared memory: 16 lanes take one 1 x 128 block
+// (experts' rows go through the tile kernel all the same).  Not timed.
 #include "fp8_quant_tile.h"
 #include "gated_act.h"
 #include "nvfp4_internal.h"

@@ -36,6 +36,9 @@
 //  * INT8, with one scale for each row of either operand: the sums are 32-bit
 //    integers that stay in the accumulators to the end, the scales are applied
 //    as the tile goes out, and a stage holds no scales.
+// Both write eight neighbouring outputs a lane: whole 16-byte pieces of aligned rows
+// (fp32 ones in pairs), else element by element.  The plain product's runs, and its
+// column a lane for rows off 16 bytes, are not theirs.
 #pragma once
 
 #include "fp8_device.h"

@@ -10,7 +10,8 @@
 // A launch takes a table of up to kPiece tensors as its argument.  All of
 // their elements, in units of kUnit, are dealt to the workgroups in equal
 // contiguous runs, so one search of the table serves a run and tensors of any
-// size keep the card busy.  Each workgroup leaves one partial sum; whoever
+// size keep the card busy (up to 2048 workgroups: two rounds of the norm's 110 registers;
+// the scaling's 66 leave 256 of them to a second one).  Each workgroup leaves one partial sum; whoever
 // needs the norm adds the partials in the same fixed order, so results do not
 // change between calls and no atomics are needed.
 #include "nvfp4_device.h"

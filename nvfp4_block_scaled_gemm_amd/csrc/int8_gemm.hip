@@ -9,7 +9,10 @@
 //
 // Many rows: the tile of the FP8 products (fp8_tile.h) without scales in its
 // loop.  Few rows or outputs: the weights are streamed, K split over a
-// workgroup's waves, as in fp8_stream.hip.
+// workgroup's waves, as in fp8_stream.hip.  There the compiler keeps a block's
+// loads together; here, where nothing waits for scales, it puts the last of them
+// behind the block's first product, so three or four 16-byte loads of a wave are in
+// flight (44 to 47 registers) and UNROLL does not add to them.  Not timed.
 #include <type_traits>
 
 #include "fp8_launch.h"
@@ -153,8 +156,9 @@ hipError_t stream_cfg(int64_t M, int64_t N, int64_t K, Int8Operand a, Int8Operan
 
 }  // namespace
 
-// The FP8 products' borders and times (fp8_stream.hip, fp8_gemm.hip), whose loads
-// and tiles these are; not timed here.  Every variant gives the same bits.
+// The FP8 products' borders and times (fp8_stream.hip, fp8_gemm.hip), whose tiles
+// these are.  None was measured with integers: those times hold the scaled additions
+// that this loop is without.  Every variant gives the same bits.
 hipError_t launch_int8_gemm(int64_t M, int64_t N, int64_t K, Int8Operand a, Int8Operand b, Fp8Out y,
                             hipStream_t stream) {
   if (M <= 16 || tiles_of(M, N, 32, 32) <= 256) {
