@@ -392,8 +392,8 @@ int nvfp4_fp8_grouped_wgrad(int32_t G, const int32_t* m_offsets, int64_t total_m
 
 /* Activation of a gated block: act(g) = g sigma(z), with z = g (SILU) or
  * z = 2 sqrt(2/pi) (g + 0.044715 g^3) (GELU, the tanh form), in fp32: sigma has
- * the bits of a subnormal number below 2^-126 and is 0 from 2^-150 on.  An infinite
- * g gives act(g) = g or (-infinity) NaN. */
+ * the bits of a subnormal number below 2^-126 and is 0 from 2^-150 on.  Of an
+ * infinite g act is g or (-infinity) NaN, and act' NaN. */
 typedef enum {
   NVFP4_SILU = 0,
   NVFP4_GELU = 1

@@ -505,3 +505,23 @@ def test_backward_rounds_as_fp32(act):
     got = np_(c[1]).astype(np.float64)[0, :8192] * 448
     want = np.abs(act_ref(g.numpy()[0], act)[1])
     assert np.linalg.norm(got - want) <= 2.1 * 2.53e-8 * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_gates_that_are_not_finite(act):
+    """act(inf) = inf, act(-inf) and act(NaN) are NaN, as is act' of all three; the blocks
+    that hold them are marked, finite gates beside them are not."""
+    inf = float("inf")
+    gate = torch.tensor([inf, -inf, float("nan"), 3e38, -3e38, 1.0, 0.0, -1.0])
+    note(f"fp8 gated, gates that are not finite, {act}")
+    for M in (2, 100):
+        q = torch.zeros(M, 128)
+        w = torch.zeros(16, 128)
+        q[:, 0] = w[:, 0] = 1
+        f8 = torch.float8_e4m3fn
+        h = nv.nvfp4_fp8_gated_gemm((q.to(f8).to(DEV), torch.ones(1, M, device=DEV)),
+                                    (w.to(f8).to(DEV), torch.cat([gate, torch.ones(8)])[None].to(DEV)), act, "f32").cpu()
+        assert (h[:, 0] == inf).all() and h[:, 1:3].isnan().all() and h[:, 3:].isfinite().all()
+    gu = torch.cat([gate, torch.ones(8)])[None]
+    _, s = nv.nvfp4_fp8_gated_backward(torch.ones(1, 8, device=DEV), gu.to(DEV), act, layout="cols")
+    assert s.cpu().isnan().tolist() == [[True] * 3 + [False] * 5 + [True] * 3 + [False] * 5]
