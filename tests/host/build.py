@@ -115,6 +115,9 @@ def build() -> str:
     os.makedirs(OUT, exist_ok=True)
     with tempfile.TemporaryDirectory(dir=OUT) as work:
         os.replace(_link(work, inputs), lib)
+    for other in glob.glob(os.path.join(OUT, "libnvfp4_host_*.so")):  # of older sources
+        if other != lib:
+            os.remove(other)
     return lib
 
 
